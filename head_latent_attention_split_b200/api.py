@@ -160,3 +160,240 @@ def sparse_decode(q_lat, q_rope, kv_cache, block_table, indices, counts, softmax
     _b.mla_sparse_decode(p, top_k, q_lat, q_rope, kv_cache, block_table, indices, counts, out, lse, workspace,
                          stream=stream)
     return out, lse
+
+
+# ---------------------------------------------------------------- window decode, eviction, draft verification
+#
+# The calls below check their tensors (device, type, shape, contiguity) before the library sees a
+# pointer, run on the tensors' device whatever the current one is, and allocate on the stream
+# they launch on.
+class _On:
+    """Context of one call: `dev` is current inside it, and `stream` (a torch stream, a raw handle
+    or None for the current one)."""
+    __slots__ = ("ctx",)
+
+    def __init__(self, dev, stream):
+        import torch
+        self.ctx = None
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+            if stream.device != dev:
+                raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
+            self.ctx = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != dev.index:
+            self.ctx = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _need(dev, what, t, dtypes, shape):
+    """t is a contiguous tensor on dev of one of `dtypes` and of `shape`."""
+    if t.device != dev:
+        raise ValueError(f"{what} is on {t.device}, expected {dev}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: unsupported dtype {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _cuda_device(t, what):
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return t.device
+
+
+def _dims(t, what, n):
+    if t.dim() != n:
+        raise ValueError(f"{what} must have {n} dimensions, got {t.dim()}")
+    return t.shape
+
+
+def _check_step(q_lat, q_rope, kv_cache, block_table, seq_lens, k_rope_cache, kv_scale):
+    """The tensors of a decode step fit one another; returns their device."""
+    import torch
+    dev = _cuda_device(q_lat, "q_lat")
+    B, Sq, H, r = _dims(q_lat, "q_lat", 4)
+    d_r = 0 if q_rope is None else _dims(q_rope, "q_rope", 4)[3]
+    nb, bs, width = _dims(kv_cache, "kv_cache", 3)
+    f32, bf16, i32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
+    fp8 = kv_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
+    qt = bf16 if fp8 else (kv_cache.dtype,)
+    _need(dev, "q_lat", q_lat, qt, (B, Sq, H, r))
+    if q_rope is not None:
+        _need(dev, "q_rope", q_rope, qt, (B, Sq, H, d_r))
+    if fp8:
+        _need(dev, "kv_cache", kv_cache, (kv_cache.dtype,), (nb, bs, r))
+        if kv_scale is None or (d_r > 0 and k_rope_cache is None):
+            raise ValueError("an e4m3 cache needs k_rope_cache and kv_scale")
+        if k_rope_cache is not None:
+            _need(dev, "k_rope_cache", k_rope_cache, bf16, (nb, bs, d_r))
+        _need(dev, "kv_scale", kv_scale, f32, (nb, bs))
+    else:
+        _need(dev, "kv_cache", kv_cache, f32 + bf16, (nb, bs, r + d_r))
+        if k_rope_cache is not None or kv_scale is not None:
+            raise ValueError("k_rope_cache and kv_scale belong to an e4m3 cache")
+    _need(dev, "block_table", block_table, i32, (B, _dims(block_table, "block_table", 2)[1]))
+    _need(dev, "seq_lens", seq_lens, i32, (B,))
+    return dev
+
+
+def window_decode(q_lat, q_rope, kv_cache, block_table, seq_lens, softmax_scale, window, sinks=0, causal=False,
+                  k_rope_cache=None, kv_scale=None, out=None, lse=None, workspace=None, out_dtype=None, num_workers=0,
+                  kernel="auto", stream=None):
+    """One MLA decode step over a sliding window and sink tokens (see mla_window_decode).
+
+    A query row with n tokens (its own the last) sees tokens t < n with t >= n - window or t < sinks.
+    Other arguments and the returned (out, lse) are decode's.
+    """
+    import torch
+    dev = _check_step(q_lat, q_rope, kv_cache, block_table, seq_lens, k_rope_cache, kv_scale)
+    p = params_for(q_lat, q_rope, kv_cache, block_table, softmax_scale, causal, out_dtype, num_workers, kernel)
+    if p.out_dtype not in (_b.F32, _b.BF16):
+        raise TypeError("out_dtype must be F32 or BF16")
+    od = torch.float32 if p.out_dtype == _b.F32 else torch.bfloat16
+    with _On(dev, stream):
+        if out is None:
+            out = torch.empty(q_lat.shape, dtype=od, device=dev)
+        else:
+            _need(dev, "out", out, (od,), q_lat.shape)
+        if lse is None:
+            lse = torch.empty(q_lat.shape[:3], dtype=torch.float32, device=dev)
+        else:
+            _need(dev, "lse", lse, (torch.float32,), q_lat.shape[:3])
+        if workspace is None:
+            workspace = torch.empty(max(_b.workspace_size(p), 1), dtype=torch.uint8, device=dev)
+        _b.mla_window_decode(p, window, sinks, q_lat, q_rope, kv_cache, k_rope_cache, kv_scale, block_table, seq_lens,
+                             out, lse, workspace)
+    return out, lse
+
+
+def attention_mass(q_lat, q_rope, kv_cache, block_table, seq_lens, lse, softmax_scale, mass, mass_in=None,
+                   causal=False, k_rope_cache=None, kv_scale=None, num_workers=0, kernel="auto", stream=None):
+    """mass[b, t] = mass_in[b, t] + the attention weight that token t receives from all query rows
+    of this step, for t < seq_lens[b] (see mla_attention_mass).
+
+    lse [B, Sq, H] is the decode's; mass float32 [B, max_seq_len]; mass_in of the same shape, or mass
+    itself to add in place, or None for zeros. Entries past a sequence's length are left as they are.
+    Returns mass.
+    """
+    import torch
+    dev = _check_step(q_lat, q_rope, kv_cache, block_table, seq_lens, k_rope_cache, kv_scale)
+    f32 = (torch.float32,)
+    _need(dev, "lse", lse, f32, q_lat.shape[:3])
+    S = _dims(mass, "mass", 2)[1]
+    _need(dev, "mass", mass, f32, (q_lat.shape[0], S))
+    if mass_in is not None and mass_in is not mass:
+        _need(dev, "mass_in", mass_in, f32, mass.shape)
+    p = params_for(q_lat, q_rope, kv_cache, block_table, softmax_scale, causal, None, num_workers, kernel)
+    with _On(dev, stream):
+        _b.mla_attention_mass(p, S, q_lat, q_rope, kv_cache, k_rope_cache, kv_scale, block_table, seq_lens, lse,
+                              mass_in, mass)
+    return mass
+
+
+def evict_select(mass, seq_lens, budget, sinks=0, recent=0, indices=None, counts=None, stream=None):
+    """The tokens that stay when every sequence is cut to `budget`: the first `sinks`, the last `recent`
+    and the heaviest between (see mla_evict_select). Returns (indices int32 [B, budget] ascending, -1
+    padded; counts int32 [B]), the list that sparse_decode and cache_compact take."""
+    import torch
+    dev = _cuda_device(mass, "mass")
+    B, S = _dims(mass, "mass", 2)
+    i32 = (torch.int32,)
+    _need(dev, "mass", mass, (torch.float32,), (B, S))
+    _need(dev, "seq_lens", seq_lens, i32, (B,))
+    with _On(dev, stream):
+        if indices is None:
+            indices = torch.empty((B, max(budget, 0)), dtype=torch.int32, device=dev)
+        else:
+            _need(dev, "indices", indices, i32, (B, budget))
+        if counts is None:
+            counts = torch.empty((B,), dtype=torch.int32, device=dev)
+        else:
+            _need(dev, "counts", counts, i32, (B,))
+        _b.mla_evict_select(_b.EvictParams(B, S, budget, sinks, recent, 0), mass, seq_lens, indices, counts)
+    return indices, counts
+
+
+def cache_compact(kv_cache, block_table, dst_block_table, indices, counts, k_rope_cache=None, kv_scale=None, mass=None,
+                  mass_out=None, stream=None):
+    """Copy the listed tokens into the (free) blocks of dst_block_table, in list order (see
+    mla_cache_compact): counts are the sequences' lengths under the new table. With mass and mass_out
+    the tokens' weights move along, and the rest of each mass_out row becomes 0. Returns None."""
+    import torch
+    dev = _cuda_device(kv_cache, "kv_cache")
+    nb, bs, width = _dims(kv_cache, "kv_cache", 3)
+    B, k = _dims(indices, "indices", 2)
+    i32, f32 = (torch.int32,), (torch.float32,)
+    _need(dev, "kv_cache", kv_cache, (torch.float32, torch.bfloat16, torch.uint8, torch.float8_e4m3fn), kv_cache.shape)
+    _need(dev, "block_table", block_table, i32, (B, _dims(block_table, "block_table", 2)[1]))
+    _need(dev, "dst_block_table", dst_block_table, i32, (B, _dims(dst_block_table, "dst_block_table", 2)[1]))
+    _need(dev, "indices", indices, i32, (B, k))
+    _need(dev, "counts", counts, i32, (B,))
+    d_r = 0
+    if k_rope_cache is not None:
+        d_r = _dims(k_rope_cache, "k_rope_cache", 3)[2]
+        _need(dev, "k_rope_cache", k_rope_cache, (torch.bfloat16,), (nb, bs, d_r))
+    if kv_scale is not None:
+        _need(dev, "kv_scale", kv_scale, f32, (nb, bs))
+    if mass is not None:
+        _need(dev, "mass", mass, f32, (B, _dims(mass, "mass", 2)[1]))
+    if mass_out is not None:
+        _need(dev, "mass_out", mass_out, f32, (B, _dims(mass_out, "mass_out", 2)[1]))
+    p = _b.CompactParams(B, width, d_r, bs, nb, block_table.shape[1], dst_block_table.shape[1],
+                         _dtype_code(kv_cache, "kv_cache"), k, 0 if mass is None else mass.shape[1],
+                         0 if mass_out is None else mass_out.shape[1], 0)
+    with _On(dev, stream):
+        _b.mla_cache_compact(p, kv_cache, k_rope_cache, kv_scale, block_table, dst_block_table, indices, counts, mass,
+                             mass_out)
+
+
+def verify_drafts(target_probs, draft_probs, draft_tokens, accept_u, sample_u, draft_lens=None, seq_lens=None,
+                  tokens=None, accepted=None, new_seq_lens=None, stream=None):
+    """Accept the longest prefix of the drafted tokens that the target's probabilities allow, and draw one
+    more token (see mla_verify_drafts).
+
+    target_probs [B, K + 1, V] and draft_probs [B, K, V] (or None: the drafts were not sampled), both
+    float32 or both bfloat16; draft_tokens int32 [B, K]; accept_u float32 [B, K] and sample_u float32
+    [B] uniform in [0, 1); draft_lens int32 [B] when sequences have fewer than K drafts. Returns (tokens
+    int32 [B, K + 1], -1 padded, accepted int32 [B]), and with seq_lens (the cache's lengths, drafts
+    included) also new_seq_lens int32 [B] without the refused drafts.
+    """
+    import torch
+    dev = _cuda_device(target_probs, "target_probs")
+    B, K1, V = _dims(target_probs, "target_probs", 3)
+    K = K1 - 1
+    pt, i32, f32 = (torch.float32, torch.bfloat16), (torch.int32,), (torch.float32,)
+    _need(dev, "target_probs", target_probs, pt, target_probs.shape)
+    if draft_probs is not None:
+        _need(dev, "draft_probs", draft_probs, (target_probs.dtype,), (B, K, V))
+    _need(dev, "draft_tokens", draft_tokens, i32, (B, K))
+    _need(dev, "accept_u", accept_u, f32, (B, K))
+    _need(dev, "sample_u", sample_u, f32, (B,))
+    for what, t in (("draft_lens", draft_lens), ("seq_lens", seq_lens), ("accepted", accepted),
+                    ("new_seq_lens", new_seq_lens)):
+        if t is not None:
+            _need(dev, what, t, i32, (B,))
+    if new_seq_lens is not None and seq_lens is None:
+        raise ValueError("new_seq_lens needs seq_lens")
+    with _On(dev, stream):
+        if tokens is None:
+            tokens = torch.empty((B, K1), dtype=torch.int32, device=dev)
+        else:
+            _need(dev, "tokens", tokens, i32, (B, K1))
+        if accepted is None:
+            accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+        if seq_lens is not None and new_seq_lens is None:
+            new_seq_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        _b.mla_verify_drafts(_b.VerifyParams(B, K, V, _dtype_code(target_probs, "target_probs"), 0), target_probs,
+                             draft_probs, draft_tokens, draft_lens, accept_u, sample_u, seq_lens, tokens, accepted,
+                             new_seq_lens)
+    return (tokens, accepted) if seq_lens is None else (tokens, accepted, new_seq_lens)

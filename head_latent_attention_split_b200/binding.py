@@ -21,13 +21,14 @@ KERNEL_NAMES = {v: k for k, v in KERNELS.items()}
 MLA_OK = 0
 STATUS = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED", 3: "MLA_ERR_ALIGNMENT",
           4: "MLA_ERR_WORKSPACE_TOO_SMALL", 5: "MLA_ERR_CUDA", 6: "MLA_ERR_BAD_BLOCK_ID",
-          7: "MLA_ERR_BAD_SEQ_LEN", 8: "MLA_ERR_TIMEOUT"}
+          7: "MLA_ERR_BAD_SEQ_LEN", 8: "MLA_ERR_TIMEOUT", 9: "MLA_ERR_BAD_INPUT"}
 
 EXPORTED = ("mla_decode_workspace_size", "mla_decode_resolve", "mla_decode", "mla_decode_timed",
             "mla_decode_host_io_workspace_size", "mla_decode_host_io", "mla_plan_host", "mla_plan_probe",
             "mla_get_device_status", "mla_status_string", "mla_abi_version", "mla_decode_noalloc",
             "mla_decode_noalloc_max_workspace", "mla_cache_append", "mla_head_gemm", "mla_dsa_index",
-            "mla_dsa_topk", "mla_sparse_decode", "mla_set_wait_timeout_ns", "mla_get_wait_timeout_ns")
+            "mla_dsa_topk", "mla_sparse_decode", "mla_set_wait_timeout_ns", "mla_get_wait_timeout_ns", "mla_window_decode",
+            "mla_attention_mass", "mla_evict_select", "mla_cache_compact", "mla_verify_drafts")
 
 
 class MlaError(RuntimeError):
@@ -67,6 +68,23 @@ class DsaParams(ctypes.Structure):
         "max_seq_len", "top_k", "causal", "reserved")]
 
 
+class EvictParams(ctypes.Structure):
+    """mla_evict_params_t."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "max_seq_len", "budget", "sinks", "recent", "reserved")]
+
+
+class CompactParams(ctypes.Structure):
+    """mla_compact_params_t."""
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "kv_rank", "rope_dim", "block_size", "num_blocks", "max_blocks_per_seq", "dst_max_blocks",
+        "cache_dtype", "list_stride", "mass_stride", "mass_out_stride", "reserved")]
+
+
+class VerifyParams(ctypes.Structure):
+    """mla_verify_params_t."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "max_drafts", "vocab", "prob_dtype", "reserved")]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built: run `python -m head_latent_attention_split_b200.build` "
@@ -95,6 +113,12 @@ def _load():
     L.mla_dsa_index.argtypes = [D, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.mla_dsa_topk.argtypes = [D, vp, vp, vp, vp, vp]
     L.mla_sparse_decode.argtypes = [P, ctypes.c_int32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    i32 = ctypes.c_int32
+    L.mla_window_decode.argtypes = [P, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.mla_attention_mass.argtypes = [P, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.mla_evict_select.argtypes = [ctypes.POINTER(EvictParams), vp, vp, vp, vp, vp]
+    L.mla_cache_compact.argtypes = [ctypes.POINTER(CompactParams), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.mla_verify_drafts.argtypes = [ctypes.POINTER(VerifyParams), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.mla_set_wait_timeout_ns.argtypes = [ctypes.c_uint64]
     L.mla_get_wait_timeout_ns.argtypes = []
     for name in EXPORTED:
@@ -338,4 +362,59 @@ def mla_sparse_decode(p: Params, top_k: int, q_lat, q_rope, kv_cache, block_tabl
                                _addr(workspace), workspace_bytes, _stream(stream))
     if check:
         _check(st, "mla_sparse_decode")
+    return st
+
+
+def mla_window_decode(p: Params, window: int, sinks: int, q_lat, q_rope, kv_cache, k_rope_cache, kv_scale, block_table,
+                      seq_lens, out, lse, workspace, workspace_bytes=None, stream=None, check=True) -> int:
+    """Raw C-ABI call of the decode over a sliding window and sink tokens."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = lib.mla_window_decode(ctypes.byref(p), int(window), int(sinks), _addr(q_lat), _addr(q_rope), _addr(kv_cache),
+                               _addr(k_rope_cache), _addr(kv_scale), _addr(block_table), _addr(seq_lens), _addr(out),
+                               _addr(lse), _addr(workspace), workspace_bytes, _stream(stream))
+    if check:
+        _check(st, "mla_window_decode")
+    return st
+
+
+def mla_attention_mass(p: Params, max_seq_len: int, q_lat, q_rope, kv_cache, k_rope_cache, kv_scale, block_table,
+                       seq_lens, lse, mass_in, mass, stream=None, check=True) -> int:
+    """Raw C-ABI call of the attention weight per cached token."""
+    st = lib.mla_attention_mass(ctypes.byref(p), int(max_seq_len), _addr(q_lat), _addr(q_rope), _addr(kv_cache),
+                                _addr(k_rope_cache), _addr(kv_scale), _addr(block_table), _addr(seq_lens), _addr(lse),
+                                _addr(mass_in), _addr(mass), _stream(stream))
+    if check:
+        _check(st, "mla_attention_mass")
+    return st
+
+
+def mla_evict_select(p: EvictParams, mass, seq_lens, indices, counts, stream=None, check=True) -> int:
+    """Raw C-ABI call of the choice of the tokens that stay in the cache."""
+    st = lib.mla_evict_select(ctypes.byref(p), _addr(mass), _addr(seq_lens), _addr(indices), _addr(counts),
+                              _stream(stream))
+    if check:
+        _check(st, "mla_evict_select")
+    return st
+
+
+def mla_cache_compact(p: CompactParams, kv_cache, k_rope_cache, kv_scale, block_table, dst_block_table, indices, counts,
+                      mass, mass_out, stream=None, check=True) -> int:
+    """Raw C-ABI call of the copy of the listed tokens into other blocks."""
+    st = lib.mla_cache_compact(ctypes.byref(p), _addr(kv_cache), _addr(k_rope_cache), _addr(kv_scale),
+                               _addr(block_table), _addr(dst_block_table), _addr(indices), _addr(counts), _addr(mass),
+                               _addr(mass_out), _stream(stream))
+    if check:
+        _check(st, "mla_cache_compact")
+    return st
+
+
+def mla_verify_drafts(p: VerifyParams, target, draft, draft_tokens, draft_lens, accept_u, sample_u, seq_lens, tokens,
+                      accepted, new_seq_lens, stream=None, check=True) -> int:
+    """Raw C-ABI call of the verification of drafted tokens."""
+    st = lib.mla_verify_drafts(ctypes.byref(p), _addr(target), _addr(draft), _addr(draft_tokens), _addr(draft_lens),
+                               _addr(accept_u), _addr(sample_u), _addr(seq_lens), _addr(tokens), _addr(accepted),
+                               _addr(new_seq_lens), _stream(stream))
+    if check:
+        _check(st, "mla_verify_drafts")
     return st

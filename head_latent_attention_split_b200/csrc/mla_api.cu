@@ -141,6 +141,8 @@ mla::DecodeArgs make_args(const mla_decode_params_t* p, int W) {
 
 }  // namespace
 
+int* mla::current_status_word() { return status_word(current_device()); }
+
 uint64_t mla::wait_timeout_ns() { return g_wait_timeout_ns.load(std::memory_order_relaxed); }
 
 extern "C" {
@@ -165,6 +167,7 @@ const char* mla_status_string(int32_t s) {
     case MLA_ERR_BAD_BLOCK_ID: return "MLA_ERR_BAD_BLOCK_ID";
     case MLA_ERR_BAD_SEQ_LEN: return "MLA_ERR_BAD_SEQ_LEN";
     case MLA_ERR_TIMEOUT: return "MLA_ERR_TIMEOUT";
+    case MLA_ERR_BAD_INPUT: return "MLA_ERR_BAD_INPUT";
     default: return "MLA_ERR_UNKNOWN";
   }
 }
@@ -192,7 +195,8 @@ namespace {
 mla_status_t decode_impl(const mla_decode_params_t* p, const void* q_lat, const void* q_rope,
                          const void* kv_cache, const void* k_rope_cache, const float* kv_scale,
                          const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
-                         void* workspace, size_t workspace_bytes, void* stream, void* const* events) {
+                         void* workspace, size_t workspace_bytes, void* stream, void* const* events,
+                         int window = 0, int sinks = 0) {
   int kernel = 0, W = 0;
   mla_status_t st = resolve(p, &kernel, &W);
   if (st) return st;
@@ -217,6 +221,8 @@ mla_status_t decode_impl(const mla_decode_params_t* p, const void* q_lat, const 
   int* status = status_word(dev);
   if (!status) return MLA_ERR_CUDA;
   mla::DecodeArgs a = make_args(p, W);
+  a.window = window < a.len_cap ? window : a.len_cap;   // 0: every token before the row
+  a.sinks = sinks < a.len_cap ? sinks : a.len_cap;
   a.q_lat = q_lat;
   a.q_rope = q_rope;
   a.cache = kv_cache;
@@ -262,6 +268,68 @@ mla_status_t mla_decode_timed(const mla_decode_params_t* p, const void* q_lat, c
   if (!events || !events[0] || !events[1] || !events[2]) return MLA_ERR_INVALID_ARG;
   return decode_impl(p, q_lat, q_rope, kv_cache, k_rope_cache, kv_scale, block_table, seq_lens, out, lse,
                      workspace, workspace_bytes, stream, events);
+}
+
+mla_status_t mla_window_decode(const mla_decode_params_t* p, int32_t window, int32_t sinks, const void* q_lat,
+                               const void* q_rope, const void* kv_cache, const void* k_rope_cache,
+                               const float* kv_scale, const int32_t* block_table, const int32_t* seq_lens, void* out,
+                               float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (window < 1 || sinks < 0) return MLA_ERR_INVALID_ARG;
+  return decode_impl(p, q_lat, q_rope, kv_cache, k_rope_cache, kv_scale, block_table, seq_lens, out, lse,
+                     workspace, workspace_bytes, stream, nullptr, window, sinks);
+}
+
+mla_status_t mla_attention_mass(const mla_decode_params_t* p, int32_t max_seq_len, const void* q_lat,
+                                const void* q_rope, const void* kv_cache, const void* k_rope_cache,
+                                const float* kv_scale, const int32_t* block_table, const int32_t* seq_lens,
+                                const float* lse, const float* mass_in, float* mass, void* stream) {
+  mla_status_t st = check_shape(p);
+  if (st) return st;
+  if (max_seq_len < 0) return MLA_ERR_INVALID_ARG;
+  const bool tc_ok = mla::mass_tc_supported(p->kv_rank, p->rope_dim, p->block_size, p->q_dtype, p->cache_dtype);
+  const bool simt_fits = p->kv_rank + p->rope_dim <= mla::kSimtMaxD;
+  int kernel = p->kernel;
+  if (kernel == MLA_KERNEL_AUTO) kernel = tc_ok ? MLA_KERNEL_TCGEN05 : MLA_KERNEL_SIMT;
+  if (kernel == MLA_KERNEL_TC_PAIR || (kernel == MLA_KERNEL_TCGEN05 && !tc_ok) ||
+      (kernel == MLA_KERNEL_SIMT && !simt_fits))
+    return MLA_ERR_UNSUPPORTED;
+  if (p->num_workers > 65535) return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)p->q_len * p->num_heads > (1 << 24)) return MLA_ERR_UNSUPPORTED;   // 32-bit row numbers
+  if (p->batch == 0 || max_seq_len == 0) return MLA_OK;
+  if (!q_lat || !kv_cache || !block_table || !seq_lens || !lse || !mass) return MLA_ERR_INVALID_ARG;
+  if (p->rope_dim > 0 && !q_rope) return MLA_ERR_INVALID_ARG;
+  if (p->cache_dtype == MLA_DTYPE_E4M3) {
+    if (!kv_scale || (p->rope_dim > 0 && !k_rope_cache)) return MLA_ERR_INVALID_ARG;
+  } else if (k_rope_cache || kv_scale) {
+    return MLA_ERR_INVALID_ARG;
+  }
+  const size_t need = kernel == MLA_KERNEL_SIMT ? 4 : 16;
+  const void* ptrs[] = {q_lat, q_rope, kv_cache, k_rope_cache, kv_scale};
+  for (const void* q : ptrs)
+    if (q && !aligned(q, need)) return MLA_ERR_ALIGNMENT;
+  const void* p4[] = {block_table, seq_lens, lse, mass_in, mass};
+  for (const void* q : p4)
+    if (q && !aligned(q, 4)) return MLA_ERR_ALIGNMENT;
+  int* status = status_word(current_device());
+  if (!status) return MLA_ERR_CUDA;
+  mla::MassArgs m{};
+  m.d = make_args(p, p->num_workers);
+  m.d.q_lat = q_lat;
+  m.d.q_rope = q_rope;
+  m.d.cache = kv_cache;
+  m.d.k_rope = (const uint16_t*)k_rope_cache;
+  m.d.kv_scale = kv_scale;
+  m.d.block_table = block_table;
+  m.d.seq_lens = seq_lens;
+  m.d.status = status;
+  if (max_seq_len < m.d.len_cap) m.d.len_cap = max_seq_len;
+  m.max_seq_len = max_seq_len;
+  m.lse = lse;
+  m.mass_in = mass_in;
+  m.mass = mass;
+  const cudaError_t e = kernel == MLA_KERNEL_SIMT ? mla::launch_mass_simt(m, (cudaStream_t)stream)
+                                                  : mla::launch_mass_tc(m, (cudaStream_t)stream);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------- host I/O

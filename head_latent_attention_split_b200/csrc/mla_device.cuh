@@ -59,6 +59,56 @@ __device__ __forceinline__ int worker_of_tile(long long x, long long T, int W) {
   return (int)(((x + 1) * (long long)W - 1) / T);
 }
 
+// Which cache blocks of a sequence make up its tile list.
+//   DenseTiles: all of them, tile i is block i.
+//   WindowTiles: those that hold a token some query row sees through the window or as a sink: the
+//     blocks of tokens [0, min(sinks, L)), then those of [lo, L), lo = the first token of the
+//     first row's window. Tile i is block i before the gap and i + gap behind it.
+struct DenseTiles {
+  int bs;
+  __device__ __forceinline__ DenseTiles(int bs_) : bs(bs_) {}
+  __device__ __forceinline__ int count(int Lc) const { return tiles_of(Lc, bs); }
+  __device__ __forceinline__ int block(int i, int) const { return i; }
+};
+
+struct WindowTiles {
+  int bs, Sq, causal, window, sinks;
+  __device__ __forceinline__ WindowTiles(const DecodeArgs& a)
+      : bs(a.bs), Sq(a.Sq), causal(a.causal), window(a.window), sinks(a.sinks) {}
+  // first token of the earliest window among the sequence's query rows
+  __device__ __forceinline__ int lo(int Lc) const {
+    const int first = causal ? max(Lc - Sq + 1, 0) : Lc;
+    return max(first - window, 0);
+  }
+  __device__ __forceinline__ int sink_tiles(int Lc) const { return tiles_of(min(sinks, Lc), bs); }
+  __device__ __forceinline__ int gap(int Lc) const { return max(lo(Lc) / bs - sink_tiles(Lc), 0); }
+  __device__ __forceinline__ int count(int Lc) const { return tiles_of(Lc, bs) - gap(Lc); }
+  __device__ __forceinline__ int block(int i, int Lc) const { return i < sink_tiles(Lc) ? i : i + gap(Lc); }
+};
+
+template <bool kWindow>
+struct TilesOf {
+  typedef DenseTiles type;
+  static __device__ __forceinline__ DenseTiles make(const DecodeArgs& a) { return DenseTiles(a.bs); }
+};
+template <>
+struct TilesOf<true> {
+  typedef WindowTiles type;
+  static __device__ __forceinline__ WindowTiles make(const DecodeArgs& a) { return WindowTiles(a); }
+};
+
+// The columns of a tile's slice [base, base + n) of tokens that a query row with n_row tokens sees:
+// [0, sink) and [first, end).
+struct WindowCols {
+  int sink, first, end;
+  __device__ __forceinline__ WindowCols(const DecodeArgs& a, int n_row, int base, int n)
+      : sink(min(max(min(a.sinks, n_row) - base, 0), n)),
+        first(min(max(n_row - a.window - base, 0), n)),
+        end(min(max(n_row - base, 0), n)) {}
+  __device__ __forceinline__ bool all(int n) const { return end == n && (first == 0 || sink == n); }
+  __device__ __forceinline__ bool sees(int j) const { return j < end && (j >= first || j < sink); }
+};
+
 struct WorkerPlan {
   long long T;      // total tiles
   int W;            // active workers, min(W, T)
@@ -69,11 +119,12 @@ struct WorkerPlan {
 };
 
 // Executed by one full warp; every lane returns the same plan.
-__device__ __forceinline__ WorkerPlan warp_plan(const int32_t* __restrict__ seq_lens, int B, int bs,
+template <class Tiles>
+__device__ __forceinline__ WorkerPlan warp_plan(const int32_t* __restrict__ seq_lens, int B, const Tiles& tiles,
                                                 int cap, int W, int w, int* status) {
   const int lane = threadIdx.x & 31;
   long long T = 0;
-  for (int b = lane; b < B; b += 32) T += tiles_of(clamp_len(__ldg(seq_lens + b), cap, status), bs);
+  for (int b = lane; b < B; b += 32) T += tiles.count(clamp_len(__ldg(seq_lens + b), cap, status));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) T += __shfl_xor_sync(0xffffffffu, T, o);
   WorkerPlan p;
@@ -87,7 +138,7 @@ __device__ __forceinline__ WorkerPlan warp_plan(const int32_t* __restrict__ seq_
   long long carry = 0;
   for (int base = 0; base < B; base += 32) {
     const int b = base + lane;
-    const int n = b < B ? tiles_of(clamp_len(__ldg(seq_lens + b), cap, status), bs) : 0;
+    const int n = b < B ? tiles.count(clamp_len(__ldg(seq_lens + b), cap, status)) : 0;
     long long incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -108,10 +159,15 @@ __device__ __forceinline__ WorkerPlan warp_plan(const int32_t* __restrict__ seq_
   return p;
 }
 
+__device__ __forceinline__ WorkerPlan warp_plan(const int32_t* __restrict__ seq_lens, int B, int bs,
+                                                int cap, int W, int w, int* status) {
+  return warp_plan(seq_lens, B, DenseTiles(bs), cap, W, w, status);
+}
+
 // One split of a sequence as seen by its worker.
 struct Segment {
   int b;
-  int tile_begin, tile_end;   // local tile range within sequence b
+  int tile_begin, tile_end;   // range of sequence b's tile list
   int first_worker, splits;   // workers touching b
   int split;                  // this worker's index among them
   int Lc;                     // clamped sequence length
@@ -119,21 +175,23 @@ struct Segment {
 
 // Iterates the segments of a worker's range. Usage:
 //   SegmentIter it(plan, ...); Segment sg; while (it.next(sg)) { ... }
-struct SegmentIter {
+template <class Tiles>
+struct SegmentIterT {
   const int32_t* seq_lens;
-  int B, bs, cap, W, w;
+  Tiles tiles;
+  int B, cap, W, w;
   int* status;
   WorkerPlan p;
   int b;
   long long P;
 
-  __device__ SegmentIter(const WorkerPlan& plan, const int32_t* sl, int B_, int bs_, int cap_, int w_, int* st)
-      : seq_lens(sl), B(B_), bs(bs_), cap(cap_), W(plan.W), w(w_), status(st), p(plan), b(plan.b0), P(plan.P0) {}
+  __device__ SegmentIterT(const WorkerPlan& plan, const int32_t* sl, int B_, const Tiles& t, int cap_, int w_, int* st)
+      : seq_lens(sl), tiles(t), B(B_), cap(cap_), W(plan.W), w(w_), status(st), p(plan), b(plan.b0), P(plan.P0) {}
 
   __device__ bool next(Segment& sg) {
     while (b < B && P < p.end) {
       const int Lc = clamp_len(__ldg(seq_lens + b), cap, status);
-      const int n = tiles_of(Lc, bs);
+      const int n = tiles.count(Lc);
       const int cur = b++;
       const long long Pb = P;
       P += n;
@@ -154,6 +212,8 @@ struct SegmentIter {
   }
 };
 
+using SegmentIter = SegmentIterT<DenseTiles>;
+
 // Physical block of tile `tile` of sequence b, validated (bad ids read block 0).
 __device__ __forceinline__ int checked_block(const int32_t* __restrict__ bt, int max_blocks, int b, int tile,
                                              int num_blocks, int* status) {
@@ -169,13 +229,15 @@ __device__ __forceinline__ int checked_block(const int32_t* __restrict__ bt, int
 // sequence's length is out of range, a block id is out of range, or (sparse decode, sel_idx set)
 // a listed position is outside the block table or maps to a bad block. Such rows are written as
 // NaN.
-__device__ __forceinline__ bool segment_poisoned(const DecodeArgs& a, int b, int t0, int t1) {
+template <class Tiles>
+__device__ __forceinline__ bool segment_poisoned(const DecodeArgs& a, const Tiles& tiles, int b, int t0, int t1) {
   const int lane = threadIdx.x & 31;
   const int L = __ldg(a.seq_lens + b);
   bool bad = L < 0 || L > a.len_cap;
   if (a.sel_idx == nullptr) {
     for (int t = t0 + lane; t < t1; t += 32) {
-      const int blk = __ldg(a.block_table + (size_t)b * a.max_blocks + t);
+      const int Lc = min(max(L, 0), a.len_cap);
+      const int blk = __ldg(a.block_table + (size_t)b * a.max_blocks + tiles.block(t, Lc));
       bad |= blk < 0 || blk >= a.num_blocks;
     }
   } else if (!bad) {

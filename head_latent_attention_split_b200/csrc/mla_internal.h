@@ -33,6 +33,7 @@ struct DecodeArgs {
   const int32_t* seq_lens;     // [B]; sparse decode: the selected token counts
   const int32_t* sel_idx;      // sparse decode only: [B, top_k] selected positions, else null
   int top_k;                   // sparse decode only: row stride of sel_idx
+  int window, sinks;           // window decode only (window >= 1): tokens a row sees at the end and at the start
   void* out;                   // [B, Sq, H, r] out_dtype
   float* lse;                  // [B, Sq, H]
   // workspace
@@ -81,9 +82,24 @@ cudaError_t launch_simt_decode(const DecodeArgs& a, cudaStream_t s);
 // Log-sum-exp merge of split partials (and the fill of empty sequences).
 cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t s);
 
+// Sticky status word of the current device (null when there is none).
+int* current_status_word();
+
 // Plan probe for tests.
 cudaError_t launch_plan_probe(const DecodeArgs& a, int32_t* token_slot, int32_t* token_worker,
                               cudaStream_t s);
+
+// Attention weight per cached token (mla_mass.cu).
+struct MassArgs {
+  DecodeArgs d;                // queries, cache, lengths (W: CTAs, 0 = one per SM); out and workspace unused
+  int max_seq_len;             // row stride of mass_in and mass
+  const float* lse;            // [B, Sq, H]
+  const float* mass_in;        // [B, max_seq_len] or null (zeros)
+  float* mass;                 // [B, max_seq_len]
+};
+bool mass_tc_supported(int r, int d_r, int block_size, int q_dtype, int cache_dtype);
+cudaError_t launch_mass_simt(const MassArgs& m, cudaStream_t s);
+cudaError_t launch_mass_tc(const MassArgs& m, cudaStream_t s);
 
 // Arguments of the paged cache append kernel (mla_append.cu).
 struct AppendArgs {

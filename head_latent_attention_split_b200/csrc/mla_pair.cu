@@ -163,7 +163,10 @@ __device__ __forceinline__ int sparse_row(const DecodeArgs& a, int b, int j, int
 // kSparse: tile t of a sequence is entries [64 t, 64 t + 64) of its selected-token list (the
 // sparse decode); tm_kv is then the cache as rows [num_blocks * 64][576] (one-row boxes of 64
 // channels, 128-byte swizzle) and the producers fetch each tile's rows with 4-row gathers.
-template <bool kSparse>
+// kWindow: the tile list holds only the blocks with sink tokens or tokens of the rows' windows
+// (WindowTiles); a row's softmax masks the tokens of those blocks that it does not see, and tokens
+// that no row sees are zeroed before the PV reads them. The pipelines are the dense ones.
+template <bool kSparse, bool kWindow>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_kv4,
                        const DecodeArgs a, const int n_rg,
@@ -178,6 +181,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int w = cluster / n_rg, rg = cluster % n_rg;
   const int cap = a.len_cap;
   volatile int* abort = &ctl.abort;
+  typedef SegmentIterT<typename TilesOf<kWindow>::type> SegIter;
+  const auto tiles = TilesOf<kWindow>::make(a);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlotsS; ++i) {
@@ -213,7 +218,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fence_mbarrier_init_cluster();
   }
   if (warp == kProducerWarp) {
-    const WorkerPlan p = warp_plan(a.seq_lens, a.B, a.bs, cap, a.W, w, a.status);
+    const WorkerPlan p = warp_plan(a.seq_lens, a.B, tiles, cap, a.W, w, a.status);
     if (lane == 0) {
       ctl.plan = p;
       prefetch_tmap(rank == 0 ? &tm_kv : &tm_kv4);
@@ -247,7 +252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // lane L fetches rows 4L .. 4L + 3 of the tile pair (entries 64 tile + 4L + m), each of the
     // slot's three 64-channel chunks with one 4-row gather: the same slot layout as the tiled
     // loads (second tile's rows right after the first's).
-    SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+    SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
     Segment sg;
     uint32_t c = 0;   // slots issued
     bool ok = true;
@@ -292,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       // (An L2 prefetch of whole blocks a few tiles ahead of these loads measured slower on
       // B200, the farther ahead the slower: the ring's own loads are the only reads.)
-      SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+      SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
       Segment sg;
       uint32_t c = 0;   // slots issued
       bool ok = true;
@@ -300,8 +305,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         prefetch_query(a, sg.b, rg);
         for (int tile = sg.tile_begin; ok && tile < sg.tile_end; tile += 2) {
           const int nt = min(2, sg.tile_end - tile);
-          const int blk0 = tile_block(a, sg.b, tile);
-          const int blk1 = nt == 2 ? tile_block(a, sg.b, tile + 1) : 0;
+          const int blk0 = tile_block(a, sg.b, tiles.block(tile, sg.Lc));
+          const int blk1 = nt == 2 ? tile_block(a, sg.b, tiles.block(tile + 1, sg.Lc)) : 0;
 #pragma unroll 1   // rolled: see the score MMA loop
           for (int g = 0; g < kChunksS / kGroupS; ++g, ++c) {
             const uint32_t slot = c % kSlotsS;
@@ -336,7 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idesc2 = idesc_bf16_f32(128, 128, false);   // a tile pair
       constexpr uint32_t idesc1 = idesc_bf16_f32(128, 64, false);    // a single tile
-      SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+      SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
       Segment sg;
       uint32_t c = 0, u = 0, seg = 0;
       bool ok = true;
@@ -386,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (rank == 0 && warp < kProducerWarp) {
     // ------------------------------------------------------------------ score CTA: softmax warps
     const float scale_log2 = a.scale_log2;
-    SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+    SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
     Segment sg;
     uint32_t t = 0, u = 0, seg = 0;   // tiles and pairs before this segment, segments
     bool ok = true;
@@ -454,7 +459,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // into the exponent's FMA below); a partial one masks the columns past the row's
           // attended tokens after scaling.
           const int valid = mine ? min(max(n_row - tile * kBS, 0), kBS) : 0;
-          const bool full = valid == kBS;
+          const WindowCols cols(a, mine ? n_row : 0, kWindow ? tiles.block(tile, sg.Lc) * kBS : 0, kBS);
+          const bool full = kWindow ? cols.all(kBS) : valid == kBS;
           float mh;
           if (full) {
             float r = __uint_as_float(v[0]);
@@ -472,7 +478,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mh = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 64; ++j) {
-              const float x = j < valid ? __uint_as_float(v[j]) * scale_log2 : -INFINITY;
+              const bool see = kWindow ? cols.sees(j) : j < valid;
+              const float x = see ? __uint_as_float(v[j]) * scale_log2 : -INFINITY;
               v[j] = __float_as_uint(x);
               mh = fmaxf(mh, x);
             }
@@ -548,7 +555,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++seg;
       }
       // log-sum-exp of the rows of this segment (the output CTA writes the values)
-      const bool poisoned = segment_poisoned(a, sg.b, sg.tile_begin, sg.tile_end);
+      const bool poisoned = segment_poisoned(a, tiles, sg.b, sg.tile_begin, sg.tile_end);
       if (valid_row && half == 0) {
         float lse_v = l_tot > 0.f ? (m_run + log2f(l_tot)) * 0.69314718055994531f : -INFINITY;
         if (!ok || poisoned) lse_v = __uint_as_float(0x7FC00000u);
@@ -565,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // PV that last read receive buffer t % kRxBufs has completed, one bulk copy moves the
     // message into the output CTA's shared memory (bytes complete on its barrier).
     if (lane == 0) {
-      SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+      SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
       Segment sg;
       uint32_t t = 0;
       bool ok = true;
@@ -594,7 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ output CTA: row gathers
     // lanes 0-15 fetch the tile's rows 4L .. 4L + 3, each half stage's four 64-channel chunks
     // with one 4-row gather each (the layout of the tiled 4-D box)
-    SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+    SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
     Segment sg;
     uint32_t h = 0;
     bool ok = true;
@@ -635,13 +642,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ output CTA: TMA producer
     if (lane == 0) {
-      SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+      SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
       Segment sg;
       uint32_t h = 0;
       bool ok = true;
       while (ok && it.next(sg)) {
         for (int tile = sg.tile_begin; ok && tile < sg.tile_end; ++tile) {
-          const int blk = tile_block(a, sg.b, tile);
+          const int blk = tile_block(a, sg.b, tiles.block(tile, sg.Lc));
 #pragma unroll 1   // rolled: see the score MMA loop
           for (int hc = 0; hc < 2; ++hc, ++h) {
             const uint32_t hs = h % kHalvesO;
@@ -669,7 +676,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 256, true);
       const uint32_t rx = smem_u32(smem + kOffRx);
-      SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+      SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
       Segment sg;
       uint32_t t = 0, h = 0;
       bool ok = true;
@@ -715,7 +722,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // thread = row; warp q works on O columns [0, 256) of its rows, warp q + 4 on [256, 512)
     const uint32_t rx = smem_u32(smem + kOffRx);
     const uint32_t col0 = 256 * half;
-    SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+    SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
     Segment sg;
     uint32_t t = 0;
     bool ok = true;
@@ -723,7 +730,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int n = sg.tile_end - sg.tile_begin;
       float inv_l = 0.f;
       if (ok) {
-        const int last_tile = (sg.Lc + kBS - 1) / kBS - 1;
+        const int last_tile = tiles.count(sg.Lc) - 1;
         const int tail = sg.Lc % kBS;
         for (int li = 0; li < n; ++li, ++t) {
           const uint32_t rb = t % kRxBufs, sb = t % kStage;
@@ -759,7 +766,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             tmem_wait_st();
           }
-          if (tile == last_tile && tail != 0) {
+          if constexpr (kWindow) {
+            // Tokens that no row sees may hold anything (NaN) as well: cache slots past the
+            // sequence end, and those of a boundary block between the sinks and the earliest
+            // window. The tile keeps columns [0, sink) and [first, end).
+            const int base = tiles.block(tile, sg.Lc) * kBS;
+            const int sink = min(max(min(a.sinks, sg.Lc) - base, 0), kBS);
+            const int first = max(min(max(tiles.lo(sg.Lc) - base, 0), kBS), sink), end = min(sg.Lc - base, kBS);
+            if (sink < first || end < kBS) {
+              const uint32_t h0 = 2 * t, h1 = 2 * t + 1;
+              ok = wait_warp(smem_u32(&ctl.ofull[h0 % kHalvesO]), (h0 / kHalvesO) & 1) &&
+                   wait_warp(smem_u32(&ctl.ofull[h1 % kHalvesO]), (h1 / kHalvesO) & 1);
+              if (!ok) break;
+              const int from = min(first, end);   // rows to zero: [sink, from) and [end, 64)
+              const int hole = from - sink, gone = hole + (kBS - end);
+              for (int i = threadIdx.x; i < 64 * gone; i += kRowThreads) {
+                const int ck = i & 7, pc = (i >> 3) & 7, k = i >> 6;
+                const int tok = k < hole ? sink + k : end + (k - hole);
+                const uint32_t hs = (ck < 4 ? h0 : h1) % kHalvesO;
+                *reinterpret_cast<uint4*>(smem + kOffRingO + hs * kHalf + (ck & 3) * kChunk + tok * 128 + pc * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+            }
+          } else if (tile == last_tile && tail != 0) {
             // cache slots past the sequence end may hold anything (NaN): zero those token rows
             // of both half stages before the PV reads them (P is 0 there, but 0 * NaN is not)
             const uint32_t h0 = 2 * t, h1 = 2 * t + 1;
@@ -781,7 +811,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (ok) ok = wait_warp(smem_u32(&ctl.pv_done[(t - 1) % kRxBufs]), ((t - 1) / kRxBufs) & 1);
       }
       // epilogue: O / l -> out (single split) or the normalised partial (several splits)
-      const bool poisoned = segment_poisoned(a, sg.b, sg.tile_begin, sg.tile_end);
+      const bool poisoned = segment_poisoned(a, tiles, sg.b, sg.tile_begin, sg.tile_end);
       const bool nan_rows = !ok || poisoned;
       const bool direct = sg.splits == 1;
       const size_t qrow = (size_t)sg.b * a.rows + grow;
@@ -885,24 +915,22 @@ cudaError_t launch_pair_decode(const DecodeArgs& a, cudaStream_t s) {
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  static std::once_flag attr_once[2][64];
+  const bool windowed = a.window > 0;
+  if (sparse && windowed) return cudaErrorInvalidValue;
+  auto kernel = sparse     ? pair_decode_kernel<true, false>
+                : windowed ? pair_decode_kernel<false, true>
+                           : pair_decode_kernel<false, false>;
+  static std::once_flag attr_once[3][64];
   int dev = 0;
   cudaGetDevice(&dev);
   cudaError_t attr_err = cudaSuccess;
-  std::call_once(attr_once[sparse ? 1 : 0][dev & 63], [&] {
-    attr_err = sparse ? cudaFuncSetAttribute(pair_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kSmemBytes)
-                      : cudaFuncSetAttribute(pair_decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kSmemBytes);
+  std::call_once(attr_once[sparse ? 1 : windowed ? 2 : 0][dev & 63], [&] {
+    attr_err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   });
   if (attr_err != cudaSuccess) return attr_err;
   const int n_rg = (a.rows + kRows - 1) / kRows;
   const dim3 grid(2 * a.W * n_rg);
-  if (sparse)
-    pair_decode_kernel<true><<<grid, kThreads, kSmemBytes, s>>>(tm, tm4, a, n_rg, wait_timeout_ns(), drain_timeout_ns());
-  else
-    pair_decode_kernel<false><<<grid, kThreads, kSmemBytes, s>>>(tm, tm4, a, n_rg, wait_timeout_ns(),
-                                                                 drain_timeout_ns());
+  kernel<<<grid, kThreads, kSmemBytes, s>>>(tm, tm4, a, n_rg, wait_timeout_ns(), drain_timeout_ns());
   return cudaGetLastError();
 }
 

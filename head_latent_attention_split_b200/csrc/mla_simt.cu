@@ -41,6 +41,7 @@ __device__ __forceinline__ void store_out(void* out, int dtype, size_t i, float 
   }
 }
 
+template <bool kWindow>
 __global__ void __launch_bounds__(kThreads) simt_decode_kernel(const DecodeArgs a, int chunk) {
   extern __shared__ float tok[];   // [chunk][D]
   __shared__ WorkerPlan s_plan;
@@ -51,15 +52,16 @@ __global__ void __launch_bounds__(kThreads) simt_decode_kernel(const DecodeArgs 
   const bool row_ok = row < a.rows;
   const int s = row_ok ? row / a.H : 0;
   const int cap = a.len_cap;
+  const auto tiles = TilesOf<kWindow>::make(a);   // windowed: only the blocks that some row sees
 
   if (warp == 0) {
-    WorkerPlan p = warp_plan(a.seq_lens, a.B, a.bs, cap, a.W, w, a.status);
+    WorkerPlan p = warp_plan(a.seq_lens, a.B, tiles, cap, a.W, w, a.status);
     if (lane == 0) s_plan = p;
   }
   __syncthreads();
   const WorkerPlan plan = s_plan;
 
-  SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+  SegmentIterT<typename TilesOf<kWindow>::type> it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
   Segment sg;
   while (it.next(sg)) {
     const int b = sg.b;
@@ -83,58 +85,72 @@ __global__ void __launch_bounds__(kThreads) simt_decode_kernel(const DecodeArgs 
     for (int i = 0; i < kAV; ++i) acc[i] = 0.f;
     float m = -INFINITY, l = 0.f;
 
-    const int t_begin = sg.tile_begin * a.bs;
-    const int t_end = min(sg.tile_end * a.bs, sg.Lc);
+    // the segment's tokens are runs of consecutive positions: one, or two around the gap
+    // between the sink blocks and the window's
     const int n_row = a.causal ? sg.Lc - a.Sq + 1 + s : sg.Lc;   // tokens this row may see
-    const int hi = min(t_end, n_row);
-
-    for (int c0 = t_begin; c0 < t_end; c0 += chunk) {
-      const int cn = min(chunk, t_end - c0);
-      __syncthreads();
-      for (int j = 0; j < cn; ++j) {
-        const int t = c0 + j;
-        const int blk = checked_block(a.block_table, a.max_blocks, b, t / a.bs, a.num_blocks, a.status);
-        const size_t slot = (size_t)blk * a.bs + (t % a.bs);
-        for (int k = threadIdx.x; k < D; k += kThreads) {
-          float v;
-          if (a.cache_dtype == kE4M3) {
-            if (k < a.r)
-              v = e4m3_to_float(__ldg((const uint8_t*)a.cache + slot * a.r + k)) * __ldg(a.kv_scale + slot);
-            else
-              v = bf16_bits_to_float(__ldg(a.k_rope + slot * a.d_r + (k - a.r)));
-          } else if (a.cache_dtype == kBF16) {
-            v = bf16_bits_to_float(__ldg((const uint16_t*)a.cache + slot * D + k));
-          } else {
-            v = __ldg((const float*)a.cache + slot * D + k);
-          }
-          tok[j * D + k] = v;
-        }
+    const int n_runs = kWindow ? 2 : 1;
+    for (int run = 0; run < n_runs; ++run) {
+      int t_begin = sg.tile_begin * a.bs, t_end = min(sg.tile_end * a.bs, sg.Lc);
+      int lo = 0, sink = 0;   // the row sees tokens t < n_row with t >= lo or t < sink
+      if constexpr (kWindow) {
+        const int st = tiles.sink_tiles(sg.Lc), gap = tiles.gap(sg.Lc);
+        const int i0 = run == 0 ? sg.tile_begin : max(sg.tile_begin, st);
+        const int i1 = run == 0 ? min(sg.tile_end, st) : sg.tile_end;
+        t_begin = (i0 + (run ? gap : 0)) * a.bs;
+        t_end = min((i1 + (run ? gap : 0)) * a.bs, sg.Lc);
+        lo = n_row - a.window;
+        sink = a.sinks;
       }
-      __syncthreads();
-      if (!row_ok) continue;
-      const int jn = min(cn, hi - c0);
-      for (int j = 0; j < jn; ++j) {
-        const float* c = tok + j * D;
-        float d = 0.f;
-#pragma unroll
-        for (int i = 0; i < kQV; ++i) {
-          const int k = lane + 32 * i;
-          if (k < D) d = fmaf(q[i], c[k], d);
+      const int hi = min(t_end, n_row);
+      for (int c0 = t_begin; c0 < t_end; c0 += chunk) {
+        const int cn = min(chunk, t_end - c0);
+        __syncthreads();
+        for (int j = 0; j < cn; ++j) {
+          const int t = c0 + j;
+          const int blk = checked_block(a.block_table, a.max_blocks, b, t / a.bs, a.num_blocks, a.status);
+          const size_t slot = (size_t)blk * a.bs + (t % a.bs);
+          for (int k = threadIdx.x; k < D; k += kThreads) {
+            float v;
+            if (a.cache_dtype == kE4M3) {
+              if (k < a.r)
+                v = e4m3_to_float(__ldg((const uint8_t*)a.cache + slot * a.r + k)) * __ldg(a.kv_scale + slot);
+              else
+                v = bf16_bits_to_float(__ldg(a.k_rope + slot * a.d_r + (k - a.r)));
+            } else if (a.cache_dtype == kBF16) {
+              v = bf16_bits_to_float(__ldg((const uint16_t*)a.cache + slot * D + k));
+            } else {
+              v = __ldg((const float*)a.cache + slot * D + k);
+            }
+            tok[j * D + k] = v;
+          }
         }
-        const float x = warp_sum(d) * a.scale_log2;
-        const float m_new = fmaxf(m, x);
-        const float corr = exp2f(m - m_new);
-        const float p = exp2f(x - m_new);
-        l = fmaf(l, corr, p);
+        __syncthreads();
+        if (!row_ok) continue;
+        const int jn = min(cn, hi - c0);
+        for (int j = 0; j < jn; ++j) {
+          if (kWindow && c0 + j < lo && c0 + j >= sink) continue;
+          const float* c = tok + j * D;
+          float d = 0.f;
 #pragma unroll
-        for (int i = 0; i < kAV; ++i) {
-          const int k = lane + 32 * i;
-          if (k < a.r) acc[i] = fmaf(acc[i], corr, p * c[k]);
+          for (int i = 0; i < kQV; ++i) {
+            const int k = lane + 32 * i;
+            if (k < D) d = fmaf(q[i], c[k], d);
+          }
+          const float x = warp_sum(d) * a.scale_log2;
+          const float m_new = fmaxf(m, x);
+          const float corr = exp2f(m - m_new);
+          const float p = exp2f(x - m_new);
+          l = fmaf(l, corr, p);
+#pragma unroll
+          for (int i = 0; i < kAV; ++i) {
+            const int k = lane + 32 * i;
+            if (k < a.r) acc[i] = fmaf(acc[i], corr, p * c[k]);
+          }
+          m = m_new;
         }
-        m = m_new;
       }
     }
-    const bool poisoned = segment_poisoned(a, b, sg.tile_begin, sg.tile_end);
+    const bool poisoned = segment_poisoned(a, tiles, b, sg.tile_begin, sg.tile_end);
     if (!row_ok) continue;
     const float qnan = __uint_as_float(0x7FC00000u);
     const float inv = poisoned ? qnan : l > 0.f ? 1.f / l : 0.f;
@@ -163,16 +179,18 @@ __global__ void __launch_bounds__(kThreads) simt_decode_kernel(const DecodeArgs 
 // workspace is trusted for indexing). Rows of a sequence with a seq_len out of range, and rows
 // whose partials carry a NaN log-sum-exp (a decode wait timed out, or a bad block id), are
 // written as NaN.
+template <bool kWindow>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
   __shared__ long long s_sum[kWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.x;
   const int cap = a.len_cap;
+  const auto tiles = TilesOf<kWindow>::make(a);
   // tiles before sequence b and in total, as the decode kernels' plan counts them
   long long before = 0, total = 0;
   for (int i = threadIdx.x; i < a.B; i += kThreads) {
     const int L = __ldg(a.seq_lens + i);
-    const long long n = tiles_of(L < 0 ? 0 : (L > cap ? cap : L), a.bs);
+    const long long n = tiles.count(L < 0 ? 0 : (L > cap ? cap : L));
     total += n;
     if (i < b) before += n;
   }
@@ -202,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
     if (lane == 0) a.lse[orow] = qnan;
     return;
   }
-  const long long n = tiles_of(raw, a.bs);
+  const long long n = tiles.count(raw);
   if (n == 0) {
     for (int k = lane; k < a.r; k += 32) store_out(a.out, a.out_dtype, orow * a.r + k, 0.f);
     if (lane == 0) a.lse[orow] = -INFINITY;
@@ -341,13 +359,15 @@ cudaError_t launch_simt_decode(const DecodeArgs& a, cudaStream_t s) {
   if (chunk > 32) chunk = 32;
   if (chunk < 1) chunk = 1;
   dim3 grid(a.W, (a.rows + kWarps - 1) / kWarps);
-  simt_decode_kernel<<<grid, kThreads, sizeof(float) * chunk * D, s>>>(a, chunk);
+  auto kernel = a.window > 0 ? simt_decode_kernel<true> : simt_decode_kernel<false>;
+  kernel<<<grid, kThreads, sizeof(float) * chunk * D, s>>>(a, chunk);
   return cudaGetLastError();
 }
 
 cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t s) {
   dim3 grid(a.B, (a.rows + kWarps - 1) / kWarps);
-  combine_kernel<<<grid, kThreads, 0, s>>>(a);
+  auto kernel = a.window > 0 ? combine_kernel<true> : combine_kernel<false>;
+  kernel<<<grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

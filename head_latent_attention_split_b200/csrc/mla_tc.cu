@@ -192,7 +192,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-template <bool kFp8, bool kSparse>
+template <bool kFp8, bool kSparse, bool kWindow>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kSparse>(), 1)
     tc_decode_kernel(const __grid_constant__ CUtensorMap tm_qr, const __grid_constant__ CUtensorMap tm_kv,
                      const __grid_constant__ CUtensorMap tm_kr, const __grid_constant__ CUtensorMap tm_sc,
@@ -212,6 +212,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
   const int w = cluster / n_rg, rg = cluster % n_rg;
   const int cap = a.len_cap;
   volatile int* abort = &ctl.abort;
+  typedef SegmentIterT<typename TilesOf<kWindow>::type> SegIter;
+  const auto tiles = TilesOf<kWindow>::make(a);   // windowed: only the blocks that some row sees
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -244,7 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
     fence_mbarrier_init_cluster();
   }
   if (warp == kProducerWarp) {
-    const WorkerPlan p = warp_plan(a.seq_lens, a.B, a.bs, cap, a.W, w, a.status);
+    const WorkerPlan p = warp_plan(a.seq_lens, a.B, tiles, cap, a.W, w, a.status);
     if (lane == 0) {
       ctl.plan = p;
       prefetch_tmap(&tm_qr);
@@ -272,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
     // four rows' 64-byte RoPE slices. Every lane's copies of a tile complete one arrival on
     // the stage barrier; rows that are not there are zero-filled without a read.
     const int half = warp == kProducerWarp ? 0 : 1;
-    SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+    SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
     Segment sg;
     uint32_t g = 0, seg = 0;
     bool ok = true;
@@ -337,7 +339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
   } else if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+      SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
       Segment sg;
       uint32_t g = 0, seg = 0;
       bool ok = true;
@@ -351,7 +353,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
           const uint32_t st = g % kStages, ph = (g / kStages) & 1;
           ok = mbar_wait<false>(smem_u32(&ctl.kv_empty[st]), ph ^ 1, abort, timeout_ns);
           if (!ok) break;
-          const int blk = checked_block(a.block_table, a.max_blocks, sg.b, tile, a.num_blocks, a.status);
+          const int blk = checked_block(a.block_table, a.max_blocks, sg.b, tiles.block(tile, sg.Lc), a.num_blocks,
+                                        a.status);
           const uint32_t bar = smem_u32(&ctl.kv_full[st]);
           const uint32_t base = sKv + st * kStageBytes;
           if constexpr (kFp8) {
@@ -384,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
       constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 64, false);
       constexpr uint32_t idesc_qk_lat = kFp8 ? idesc_f16_f32(128, 64, false) : idesc_qk;
       constexpr uint32_t idesc_pv = kFp8 ? idesc_f16_f32(128, 256, true) : idesc_bf16_f32(128, 256, true);
-      SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+      SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
       Segment sg;
       uint32_t g = 0, seg = 0;
       bool ok = true;
@@ -456,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
     // ------------------------------------------------------------------ FP8 converters
     if constexpr (kFp8) {
       const int tok = threadIdx.x - kConvWarp0 * 32;     // token row of the tile, 0..63
-      SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+      SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
       Segment sg;
       uint32_t g = 0;
       bool ok = true;
@@ -561,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
     const bool valid_row = grow < a.rows;
     const int s_idx = valid_row ? grow / a.H : 0;
     const float scale_log2 = a.scale_log2;
-    SegmentIter it(plan, a.seq_lens, a.B, a.bs, cap, w, a.status);
+    SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
     Segment sg;
     uint32_t g = 0, seg = 0;
     bool ok = true;
@@ -641,7 +644,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
         mbar_arrive(smem_u32(&ctl.q_full));
       }
       const int n = sg.tile_end - sg.tile_begin;
-      const int last_tile = (sg.Lc + kBS - 1) / kBS - 1;
+      const int last_tile = tiles.count(sg.Lc) - 1;
       float m_run = -INFINITY, l_run = 0.f;   // own rows: running maximum (log2 units), this thread's sum
       if (own) {
         int n_row = valid_row ? (a.causal ? sg.Lc - a.Sq + 1 + s_idx : sg.Lc) : 0;
@@ -660,6 +663,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
           float x[32];
           float mh = -INFINITY;
           const int valid = min(max(n_row - tile * kBS - 32 * hf, 0), 32);   // of my 32 columns
+          const WindowCols cols(a, n_row, kWindow ? tiles.block(tile, sg.Lc) * kBS + 32 * hf : 0, 32);
+          auto sees = [&](int k) { return kWindow ? cols.sees(k) : k < valid; };
           const float4* cs = nullptr;   // FP8: token scales of my columns
           if constexpr (kFp8) {
             const uint32_t stg = gt % kStages;
@@ -687,7 +692,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
             for (int i = 0; i < 4; ++i) {
               const int k = 4 * c + i;
               const float sc = (__uint_as_float(sv[k]) + r4[i]) * c4[i] * scale_log2;
-              x[k] = k < valid ? sc : -INFINITY;
+              x[k] = sees(k) ? sc : -INFINITY;
               mh = fmaxf(mh, x[k]);
             }
           }
@@ -726,10 +731,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               const float4 v = cs[c];
-              pcs[4 * c] = 4 * c < valid ? v.x : 0.f;
-              pcs[4 * c + 1] = 4 * c + 1 < valid ? v.y : 0.f;
-              pcs[4 * c + 2] = 4 * c + 2 < valid ? v.z : 0.f;
-              pcs[4 * c + 3] = 4 * c + 3 < valid ? v.w : 0.f;
+              pcs[4 * c] = sees(4 * c) ? v.x : 0.f;
+              pcs[4 * c + 1] = sees(4 * c + 1) ? v.y : 0.f;
+              pcs[4 * c + 2] = sees(4 * c + 2) ? v.z : 0.f;
+              pcs[4 * c + 3] = sees(4 * c + 3) ? v.w : 0.f;
             }
           }
 #pragma unroll
@@ -771,7 +776,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
           // Slots past the sequence end in its last block may hold anything (NaN): zero
           // those token rows of this CTA's latent slice before the PV reads them.
           const int tail = sg.Lc % kBS;
-          if (tile == last_tile && tail != 0) {
+          if constexpr (kWindow) {
+            // ... and so may the tokens of a boundary block between the sinks and the earliest
+            // window, which no row sees. The tile keeps columns [0, sink) and [first, end).
+            const int t0 = tiles.block(tile, sg.Lc) * kBS;
+            const int sink = min(max(min(a.sinks, sg.Lc) - t0, 0), kBS);
+            const int first = max(min(max(tiles.lo(sg.Lc) - t0, 0), kBS), sink), end = min(sg.Lc - t0, kBS);
+            if (sink < first || end < kBS) {
+              const uint32_t stg = gt % kStages;
+              ok = wait_local(smem_u32(kFp8 ? &ctl.kv_ready[stg] : &ctl.kv_full[stg]), (gt / kStages) & 1);
+              if (!ok) break;
+              uint8_t* base = smem + kOffKv + stg * kStageBytes;
+              const int from = min(first, end);   // rows to zero: [sink, from) and [end, 64)
+              const int hole = from - sink, gone = hole + (kBS - end);
+              for (int i = threadIdx.x; i < 32 * gone; i += 128) {   // the 4 own warps
+                const int chunk = i & 3, pc = (i >> 2) & 7, k = i >> 5;
+                const int tok = k < hole ? sink + k : end + (k - hole);
+                *reinterpret_cast<uint4*>(base + chunk * kKvLatChunk + tok * 128 + pc * 16) = make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+            }
+          } else if (tile == last_tile && tail != 0) {
             const uint32_t stg = gt % kStages;
             ok = wait_local(smem_u32(kFp8 ? &ctl.kv_ready[stg] : &ctl.kv_full[stg]), (gt / kStages) & 1);
             if (!ok) break;
@@ -894,7 +919,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
         __syncwarp();
         if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.lrx_full[seg & 1]), kLrxBytes);   // segment seg + 2
       }
-      const bool poisoned = segment_poisoned(a, sg.b, sg.tile_begin, sg.tile_end);
+      const bool poisoned = segment_poisoned(a, tiles, sg.b, sg.tile_begin, sg.tile_end);
       const float inv = poisoned ? __uint_as_float(0x7FC00000u) : l_tot > 0.f ? 1.f / l_tot : 0.f;
       const size_t qrow = (size_t)sg.b * a.rows + grow;
       const bool direct = sg.splits == 1;
@@ -1051,31 +1076,25 @@ cudaError_t launch_tc_decode(const DecodeArgs& a, cudaStream_t s) {
   }
   if (!ok) return cudaErrorInvalidValue;
   if (!fp8) tsc = tkr;   // unused by the bf16 kernels
-  static std::once_flag attr_once[3][64];
+  const bool windowed = a.window > 0;
+  if (sparse && windowed) return cudaErrorInvalidValue;
+  auto kernel = sparse          ? tc_decode_kernel<false, true, false>
+                : fp8 && windowed ? tc_decode_kernel<true, false, true>
+                : fp8             ? tc_decode_kernel<true, false, false>
+                : windowed        ? tc_decode_kernel<false, false, true>
+                                  : tc_decode_kernel<false, false, false>;
+  const int smem = fp8 ? Geo<true>::kSmemBytes : Geo<false>::kSmemBytes;
+  const int threads = sparse ? threads_for<false, true>() : fp8 ? threads_for<true, false>() : threads_for<false, false>();
+  static std::once_flag attr_once[5][64];
   int dev = 0;
   cudaGetDevice(&dev);
-  const int variant = sparse ? 2 : fp8 ? 1 : 0;
+  const int variant = sparse ? 2 : (fp8 ? 1 : 0) + (windowed ? 3 : 0);
   cudaError_t attr_err = cudaSuccess;
-  std::call_once(attr_once[variant][dev & 63], [&] {
-    attr_err = variant == 1 ? cudaFuncSetAttribute(tc_decode_kernel<true, false>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<true>::kSmemBytes)
-               : variant == 2 ? cudaFuncSetAttribute(tc_decode_kernel<false, true>,
-                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<false>::kSmemBytes)
-                              : cudaFuncSetAttribute(tc_decode_kernel<false, false>,
-                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<false>::kSmemBytes);
-  });
+  std::call_once(attr_once[variant][dev & 63],
+                 [&] { attr_err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (attr_err != cudaSuccess) return attr_err;
-  const uint64_t timeout_ns = wait_timeout_ns(), drain_ns = drain_timeout_ns();
   const dim3 grid(2 * a.W * n_rg);
-  if (variant == 1)
-    tc_decode_kernel<true, false><<<grid, threads_for<true, false>(), Geo<true>::kSmemBytes, s>>>(tqr, tkv, tkr, tsc, a, n_rg,
-                                                                                           timeout_ns, drain_ns);
-  else if (variant == 2)
-    tc_decode_kernel<false, true><<<grid, threads_for<false, true>(), Geo<false>::kSmemBytes, s>>>(tqr, tkv, tkr, tsc, a,
-                                                                                             n_rg, timeout_ns, drain_ns);
-  else
-    tc_decode_kernel<false, false><<<grid, threads_for<false, false>(), Geo<false>::kSmemBytes, s>>>(tqr, tkv, tkr, tsc, a,
-                                                                                              n_rg, timeout_ns, drain_ns);
+  kernel<<<grid, threads, smem, s>>>(tqr, tkv, tkr, tsc, a, n_rg, wait_timeout_ns(), drain_timeout_ns());
   return cudaGetLastError();
 }
 

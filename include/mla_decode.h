@@ -85,7 +85,9 @@ typedef enum {
   MLA_ERR_CUDA = 5,                /* CUDA runtime / launch error */
   MLA_ERR_BAD_BLOCK_ID = 6,        /* device-detected, sticky */
   MLA_ERR_BAD_SEQ_LEN = 7,         /* device-detected, sticky */
-  MLA_ERR_TIMEOUT = 8              /* device-detected bounded wait expiry, sticky */
+  MLA_ERR_TIMEOUT = 8,             /* device-detected bounded wait expiry, sticky */
+  MLA_ERR_BAD_INPUT = 9            /* device-detected, sticky: a token id, draft count or probability row that
+                                      mla_verify_drafts cannot use */
 } mla_status_t;
 
 typedef enum {
@@ -364,6 +366,140 @@ mla_status_t mla_sparse_decode(const mla_decode_params_t* params, int32_t top_k,
                                const void* q_rope, const void* kv_cache, const int32_t* block_table,
                                const int32_t* indices, const int32_t* counts, void* out, float* lse,
                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ window decode
+ *
+ * mla_decode over a sliding window and a few first tokens that stay visible (sinks): query row
+ * s of sequence b sees token t when
+ *     t < n_s  and  (t < sinks  or  t >= n_s - window),
+ *     n_s = seq_lens[b] (causal == 0)  or  seq_lens[b] - Sq + 1 + s (causal != 0),
+ * so a row's window holds its last `window` tokens, its own included, and a sink inside the window
+ * counts once. window >= 1, sinks >= 0; values past the block table's capacity act as the
+ * capacity (a window of at least the sequence's length is mla_decode). out, lse, the other
+ * arguments, the workspace (mla_decode_workspace_size of the same params), the kernels and the
+ * handling of bad lengths and blocks are mla_decode's; the sequences' RoPE keys keep the
+ * positions they were rotated for. Blocks that hold no token any row sees are not read and
+ * their block ids are not checked. Tokens that no row of the sequence sees may hold anything (NaN
+ * included); a token that some row sees has to be finite, as in mla_decode. */
+mla_status_t mla_window_decode(const mla_decode_params_t* params, int32_t window, int32_t sinks,
+                               const void* q_lat, const void* q_rope, const void* kv_cache,
+                               const void* k_rope_cache, const float* kv_scale, const int32_t* block_table,
+                               const int32_t* seq_lens, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ attention weight and eviction
+ *
+ * mla_attention_mass adds up the attention that every cached token receives in a decode step:
+ *
+ *     mass[b,t] = mass_in[b,t] + sum over the rows (s, h) that see token t of
+ *                                exp(sigma_t(s,h) - lse[b,s,h]),        t < seq_lens[b],
+ *
+ * with mla_decode's scores, causal rule and lse output (so each row adds 1 over the sequence). All
+ * sums are fp32, in a fixed order. mass_in may be NULL (zeros) or equal mass; entries
+ * t >= seq_lens[b] are not written. mass_in, mass f32 [B, max_seq_len]; lse f32 [B, Sq, H].
+ * params: as for mla_decode (out_dtype is not used; kernel AUTO, SIMT or TCGEN05; num_workers
+ * is the number of CTAs of the TCGEN05 kernel, 0 = one per SM). A seq_len above max_seq_len
+ * or the block table's capacity sets MLA_ERR_BAD_SEQ_LEN and skips the sequence; tokens of a
+ * block id out of range get NaN and set MLA_ERR_BAD_BLOCK_ID. Asynchronous, allocates nothing.
+ *
+ * TCGEN05 with an E4M3 cache multiplies the codes as they are and splits each bf16 query value
+ * into two e4m3 terms, x = hi + lo, scaled by a power of two per row: exact for values within
+ * 2^-10 of the row's largest magnitude, off by at most 2^-18 of that magnitude below it. */
+mla_status_t mla_attention_mass(const mla_decode_params_t* params, int32_t max_seq_len, const void* q_lat,
+                                const void* q_rope, const void* kv_cache, const void* k_rope_cache,
+                                const float* kv_scale, const int32_t* block_table, const int32_t* seq_lens,
+                                const float* lse, const float* mass_in, float* mass, void* stream);
+
+/* mla_evict_select picks the tokens of every sequence that stay in the cache: all of them when
+ * seq_lens[b] <= budget, else the first `sinks`, the last `recent` and, of the tokens between,
+ * the budget - sinks - recent with the largest mass (equal masses: the lower position; -0 equals
+ * +0; a NaN ranks above every number). indices int32 [B, budget] gets the positions in ascending
+ * order, -1 past the count; counts int32 [B] = min(seq_lens[b], budget): the list format of
+ * mla_sparse_decode, which can attend over the kept tokens without moving them. mass f32
+ * [B, max_seq_len]. sinks + recent <= budget, budget >= 1. A seq_len below 0 or above max_seq_len
+ * sets MLA_ERR_BAD_SEQ_LEN and counts as 0. Asynchronous, allocates nothing. */
+typedef struct {
+  int32_t batch;        /* B */
+  int32_t max_seq_len;  /* row stride of mass */
+  int32_t budget;       /* tokens to keep; row stride of indices */
+  int32_t sinks;        /* first tokens that always stay */
+  int32_t recent;       /* last tokens that always stay */
+  int32_t reserved;     /* must be 0 */
+} mla_evict_params_t;
+
+mla_status_t mla_evict_select(const mla_evict_params_t* params, const float* mass, const int32_t* seq_lens,
+                              int32_t* indices, int32_t* counts, void* stream);
+
+/* mla_cache_compact copies the listed tokens of every sequence into other blocks of the same
+ * pool: entry j < counts[b] of indices[b] moves from the slot block_table maps it to, to slot j
+ * through dst_block_table, with its latent, RoPE key and scale, byte for byte. When mass is
+ * given, mass_out[b, j] = mass[b, indices[b,j]] and the rest of the row (counts[b] <= j <
+ * mass_out_stride) becomes 0, so tokens appended later start without weight. counts[b] is the
+ * sequence's length under the new table; slots past it are left as they were.
+ * The blocks of dst_block_table must be free: none of them may be named by a block table that
+ * is still read (a shared prefix block can therefore stay shared with other sequences), and no two
+ * sequences may share one. The copies run in no particular order.
+ * Cache tensors and dtypes as in mla_decode; indices int32 [B, list_stride]; counts outside
+ * [0, list_stride] are clamped and set MLA_ERR_BAD_SEQ_LEN; an entry whose position or block is
+ * out of range is not copied, its mass becomes NaN, and MLA_ERR_BAD_BLOCK_ID is set.
+ * Asynchronous, allocates nothing. */
+typedef struct {
+  int32_t batch;            /* B */
+  int32_t kv_rank;          /* r */
+  int32_t rope_dim;         /* d_r */
+  int32_t block_size;
+  int32_t num_blocks;
+  int32_t max_blocks_per_seq;  /* row stride of block_table */
+  int32_t dst_max_blocks;      /* row stride of dst_block_table; dst_max_blocks * block_size >= list_stride */
+  int32_t cache_dtype;         /* mla_dtype_t */
+  int32_t list_stride;         /* row stride of indices */
+  int32_t mass_stride;         /* row stride of mass (when given) */
+  int32_t mass_out_stride;     /* row stride of mass_out, >= list_stride (when given) */
+  int32_t reserved;            /* must be 0 */
+} mla_compact_params_t;
+
+mla_status_t mla_cache_compact(const mla_compact_params_t* params, void* kv_cache, void* k_rope_cache,
+                               float* kv_scale, const int32_t* block_table, const int32_t* dst_block_table,
+                               const int32_t* indices, const int32_t* counts, const float* mass, float* mass_out,
+                               void* stream);
+
+/* ------------------------------------------------------------------ draft verification
+ *
+ * The step after a decode of several causal query tokens (Sq = K + 1: one committed token and K
+ * drafted ones): speculative sampling's accept / reject with given random numbers. With target
+ * probabilities p_i (row i of sequence b; row K follows the last draft), draft probabilities q_i
+ * and drafted tokens x_i, i < n_b = draft_lens[b] (K when draft_lens is NULL):
+ *
+ *     accepted[b] = the first i with not (accept_u[b,i] * q_i(x_i) < p_i(x_i)), n_b if there is none
+ *     tokens[b]   = x_0 .. x_{accepted-1}, then one token drawn from w, then -1
+ *     w           = max(p_i - q_i, 0) at i = accepted < n_b (p_i itself when that is 0 everywhere),
+ *                   p_{n_b} when all drafts are accepted
+ *     the draw    = the lowest t with w_0 + .. + w_t > sample_u[b] * (sum of w)
+ *     new_seq_lens[b] = seq_lens[b] - n_b + accepted[b]   (the refused drafts leave the cache)
+ *
+ * Products, differences and sums are fp64 (the sums in a fixed order). draft NULL: the drafts were
+ * not sampled (greedy, n-gram), q_i is 1 at x_i and 0 elsewhere. w counts as 0 where it is not
+ * above 0 (NaN included). sample_u is clamped into [0, 1): a value of 1 or more draws the last
+ * token with a weight, a negative or NaN one the first. Rows past i = accepted are not read.
+ * target [B, K + 1, V], draft [B, K, V] of type prob_dtype (F32 or BF16); draft_tokens int32
+ * [B, K]; accept_u f32 [B, K]; sample_u f32 [B]; tokens int32 [B, K + 1]; accepted int32 [B];
+ * seq_lens and new_seq_lens int32 [B], both or neither. new_seq_lens may equal seq_lens.
+ * A draft_lens entry outside [0, K], a token x_i outside [0, V) at i = accepted or before, and a w
+ * whose sum is 0 or not finite set MLA_ERR_BAD_INPUT; that sequence's tokens are -1, accepted is
+ * -1 and new_seq_lens counts no draft as accepted (a bad draft_lens: it is seq_lens).
+ * Asynchronous, allocates nothing. */
+typedef struct {
+  int32_t batch;       /* B */
+  int32_t max_drafts;  /* K >= 0 */
+  int32_t vocab;       /* V >= 1 */
+  int32_t prob_dtype;  /* MLA_DTYPE_F32 or MLA_DTYPE_BF16 */
+  int32_t reserved;    /* must be 0 */
+} mla_verify_params_t;
+
+mla_status_t mla_verify_drafts(const mla_verify_params_t* params, const void* target, const void* draft,
+                               const int32_t* draft_tokens, const int32_t* draft_lens, const float* accept_u,
+                               const float* sample_u, const int32_t* seq_lens, int32_t* tokens,
+                               int32_t* accepted, int32_t* new_seq_lens, void* stream);
 
 /* MLA_DECODE_ABI_VERSION of the loaded library. */
 int32_t mla_abi_version(void);
