@@ -5,14 +5,36 @@
 // of one sequence, decoded to fp32 in shared memory; lane = token, a warp takes every eighth group
 // of four query rows, so one token value serves four products. Bound by the fp32 products (and the
 // shared-memory reads that feed them); it serves the shapes the tensor kernel does not take.
+//
+// mass_tc_kernel (r = 512, d_r = 64, 64-token blocks, bf16 or e4m3 cache): one pass over the cache on
+// the tensor cores, persistent, one CTA per SM on a contiguous range of 128-token tiles. The TOKENS
+// are the MMA's M = 128 and the query rows its N (up to 128), so a TMEM lane holds one token's
+// scores of all rows and the thread that reads it sums exp2(score - lse) alone: no exchange
+// between threads, one coalesced store. The query (9 chunks of 64 channels, 147 KB at 128 rows) stays
+// in shared memory for a whole run of tiles, and what is left of shared memory is a ring of 16 KB
+// cache chunks (two TMA boxes, one per block) in flight. More than 128 rows go in groups, over
+// runs of four tiles at a time (150 * 4 * 147 KB: the second group's reads hit L2); a token's sum over
+// the groups is added up by one thread, in order.
+// With an e4m3 cache the codes are an operand as they are (kind::f8f6f4): the bf16 query is split into
+// two e4m3 terms (8 = 4 + 4 significant bits, see split_row), both multiplied into one accumulator,
+// and the RoPE part has its own bf16 MMAs and accumulator since the token's scale does not apply to
+// it. No conversion of cache data at all.
+// Bound: memory. Per 128 tokens and SM 36 MMAs of N = 128 take about 2.5 k cycles and the
+// exponentials about 1.1 k (16 per cycle), the tile's bytes at 1/148 of the HBM rate 6.4 k (bf16)
+// or 3.6 k (e4m3).
+#include <cuda.h>
+
 #include <algorithm>
 #include <cmath>
 #include <mutex>
 
 #include "mla_device.cuh"
+#include "ptx_sm100.cuh"
 
 namespace mla {
 namespace {
+
+using namespace ptx;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
@@ -93,10 +115,466 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const MassArgs m) {
   }
 }
 
+// ------------------------------------------------------------------------ tensor cores
+constexpr int kR = 512, kDR = 64, kBS = 64;
+constexpr int kTile = 128;                       // tokens per tile = MMA M: two cache blocks
+constexpr uint32_t kBox = kBS * 128;             // 64 tokens x 128 bytes, 128-byte swizzle
+constexpr uint32_t kSlot = 2 * kBox;             // one chunk of a tile
+constexpr int kMaxSlots = 12;
+constexpr int kQChunks = 9;                      // query: 9 x [N rows][128 bytes]
+constexpr int kGroupRows = 128;                  // query rows per group (at most)
+constexpr int kGroupRun = 4;                     // tiles per run when there are several groups
+constexpr int kTcThreads = 320;                  // warps 0-3 sums, 4 TMA, 5 MMA, 6-9 query split (e4m3)
+constexpr int kTmaWarp = 4, kMmaWarp = 5, kSplitWarp = 6;
+constexpr uint32_t kCtlBytes = 2048;             // leaves 5 ring slots at 128 rows
+constexpr uint32_t kSmemMax = 232448;
+
+struct MassCtl {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t q_full[kQChunks], q_empty[kQChunks];   // e4m3: [0] the split latent part, [8] the RoPE part
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  WorkerPlan plan;
+  float l2[kGroupRows];      // lse * log2(e) of the group's rows; +inf for rows that are none
+  float a2[kGroupRows];      // e4m3: the row's power of two * scale * log2(e)
+  uint8_t pow2[kGroupRows];  // e4m3: exponent field of the row's power of two (split warps -> sum warps)
+};
+static_assert(sizeof(MassCtl) <= kCtlBytes, "control block");
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void e4m3x2_to_f32(uint32_t c, float& lo, float& hi) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+  asm("{.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}" : "=f"(lo), "=f"(hi) : "r"(h));
+}
+
+// One query row (16 channels per lane, v = 8 bf16 pairs) as hi + lo e4m3 terms of x * 2^-e, 2^e chosen
+// so that the largest magnitude lands in [128, 256). A bf16 value has 8 significant bits: hi is the
+// nearest value with 4, and x - hi is a multiple of the same last place with at most 4 of its own, so
+// x = hi + lo exactly down to 2^-10 of the row's largest magnitude (below, lo meets e4m3's
+// smallest step and the error is at most 2^-10 / 128 = 2^-17 of it, 2^-18 for the nearest). Returns the
+// exponent field of 2^e.
+__device__ __forceinline__ uint32_t split_row(const uint32_t* v, uint32_t* hi, uint32_t* lo) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(v[i] << 16)), fabsf(__uint_as_float(v[i] & 0xFFFF0000u))));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  // exponent field of the largest magnitude (at least 2^-100, so that 2^-e stays finite)
+  const int e = max((int)(__float_as_uint(m) >> 23), 27) - 127 - 7;
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h = 0, l = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t w = v[2 * i + j];
+      const float x0 = __uint_as_float(w << 16) * down, x1 = __uint_as_float(w & 0xFFFF0000u) * down;
+      const uint32_t c = e4m3x2(x0, x1);
+      float h0, h1;
+      e4m3x2_to_f32(c, h0, h1);
+      h |= c << (16 * j);
+      l |= e4m3x2(x0 - h0, x1 - h1) << (16 * j);
+    }
+    hi[i] = h;
+    lo[i] = l;
+  }
+  return (uint32_t)(127 + e);
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
+                   const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_kr,
+                   const MassArgs m, const int N, const int slots, const uint64_t timeout_ns, const uint64_t drain_ns) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const DecodeArgs& a = m.d;
+  const uint32_t q_chunk = (uint32_t)N * 128;            // bytes of one query chunk
+  const uint32_t sRing = smem_u32(smem), sQ = sRing + (uint32_t)slots * kSlot;
+  uint8_t* gQ = smem + (uint32_t)slots * kSlot;
+  MassCtl& ctl = *reinterpret_cast<MassCtl*>(gQ + kQChunks * q_chunk);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort = &ctl.abort;
+  constexpr int kChunks = kFp8 ? 5 : 9;                  // cache chunks per tile, the last one RoPE
+  constexpr uint32_t kTmemCols = kFp8 ? 512 : 256;       // two accumulator stages
+  constexpr uint32_t kAccCols = kTmemCols / 2;
+  constexpr float kLog2e = 1.4426950408889634f;
+  const DenseTiles tiles(kTile);
+  const int n_groups = (a.rows + kGroupRows - 1) / kGroupRows;
+
+  if (warp == kTmaWarp) {
+    const WorkerPlan p = warp_plan(a.seq_lens, a.B, tiles, a.len_cap, a.W, blockIdx.x, a.status);
+    if (lane == 0) {
+      ctl.plan = p;
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_kv);
+    }
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < slots; ++i) {
+      mbar_init(smem_u32(&ctl.full[i]), 1);
+      mbar_init(smem_u32(&ctl.empty[i]), 1);
+    }
+    for (int i = 0; i < kQChunks; ++i) {
+      mbar_init(smem_u32(&ctl.q_full[i]), kFp8 && i == 0 ? 4 : 1);   // e4m3: one arrival per split warp
+      // e4m3: the split warps also wait for the sum warps to have read the item's powers of two, which
+      // keeps q_full[0] at most one phase ahead of them
+      mbar_init(smem_u32(&ctl.q_empty[i]), kFp8 && i == 0 ? 2 : 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctl.acc_full[i]), 1);
+      mbar_init(smem_u32(&ctl.acc_empty[i]), 4);   // one arrival per sum warp
+    }
+    mbar_init(smem_u32(&ctl.drain), 1);
+    ctl.abort = 0;
+    fence_mbarrier_init_cluster();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&ctl.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem_base;
+
+  // The CTA's items in order, the same walk in every role: f(b, Lc, group, first tile, end tile) for
+  // a run of tiles of one sequence and one group of rows. Sequences with a bad length have none.
+  auto for_items = [&](auto&& f) {
+    SegmentIterT<DenseTiles> it(ctl.plan, a.seq_lens, a.B, tiles, a.len_cap, blockIdx.x, a.status);
+    Segment sg;
+    bool ok = true;
+    while (ok && it.next(sg)) {
+      const int L = __ldg(a.seq_lens + sg.b);
+      if (L < 0 || L > a.len_cap) continue;
+      const int run = n_groups == 1 ? sg.tile_end - sg.tile_begin : kGroupRun;
+      for (int t0 = sg.tile_begin; ok && t0 < sg.tile_end; t0 += run)
+        for (int g = 0; ok && g < n_groups; ++g) ok = f(sg.b, sg.Lc, g, t0, min(t0 + run, sg.tile_end));
+    }
+    return ok;
+  };
+
+  if (warp == kTmaWarp) {
+    // ---------------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      int slot = 0, issued = 0;
+      uint32_t phase = 0, item = 0, q_issued = 0;   // query chunks loaded so far
+      const bool ok = for_items([&](int b, int Lc, int g, int t0, int t1) {
+        for (int t = t0; t < t1; ++t) {
+          int blk[2];
+          const int nblk = min(tiles_of(Lc, kBS) - 2 * t, 2);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            blk[h] = h < nblk ? __ldg(a.block_table + (size_t)b * a.max_blocks + 2 * t + h) : 0;
+            if (blk[h] < 0 || blk[h] >= a.num_blocks) blk[h] = a.num_blocks;   // past the cache: reads zeros
+          }
+#pragma unroll 1
+          for (int j = 0; j < kChunks; ++j) {
+            const bool rope = j == kChunks - 1;
+            if (t == t0 && (!kFp8 || rope)) {   // the item's query chunk (e4m3: the split warps write the latent part)
+              const int qj = rope ? kQChunks - 1 : j;
+              if (!mbar_wait<false>(smem_u32(&ctl.q_empty[qj]), (item & 1) ^ 1, abort, timeout_ns)) return false;
+              const uint32_t bar = smem_u32(&ctl.q_full[qj]);
+              mbar_arrive_expect_tx(bar, q_chunk);
+              tma_load_3d(sQ + qj * q_chunk, rope ? &tm_qr : &tm_q, bar, rope ? 0 : 64 * j, g * kGroupRows, b);
+              ++q_issued;
+            }
+            if (!mbar_wait<false>(smem_u32(&ctl.empty[slot]), phase ^ 1, abort, timeout_ns)) return false;
+            const uint32_t bar = smem_u32(&ctl.full[slot]);
+            mbar_arrive_expect_tx(bar, nblk * kBox);
+            for (int h = 0; h < nblk; ++h) {
+              const uint32_t dst = sRing + slot * kSlot + h * kBox;
+              if constexpr (kFp8) {
+                if (rope)
+                  tma_load_3d(dst, &tm_kr, bar, 0, 0, blk[h]);
+                else
+                  tma_load_3d(dst, &tm_kv, bar, 128 * j, 0, blk[h]);
+              } else {
+                tma_load_3d(dst, &tm_kv, bar, 64 * j, 0, blk[h]);
+              }
+            }
+            ++issued;
+            if (++slot == slots) {
+              slot = 0;
+              phase ^= 1;
+            }
+          }
+        }
+        ++item;
+        return true;
+      });
+      // every load issued lands before the CTA may exit
+      int dummy = 0;
+      for (int i = max(0, issued - slots); i < issued; ++i)
+        mbar_wait<false>(smem_u32(&ctl.full[i % slots]), (i / slots) & 1, &dummy, drain_ns);
+      if (!ok) {   // the query chunks of an unfinished item too
+        constexpr uint32_t per = kFp8 ? 1 : kQChunks;
+        for (uint32_t i = q_issued > per ? q_issued - per : 0; i < q_issued; ++i)
+          mbar_wait<false>(smem_u32(&ctl.q_full[kFp8 ? kQChunks - 1 : i % per]), (i / per) & 1, &dummy, drain_ns);
+        set_status(a.status, MLA_ERR_TIMEOUT);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc16 = idesc_bf16_f32(kTile, N, false), idesc8 = idesc_e4m3_f32(kTile, N);
+      int slot = 0;
+      uint32_t phase = 0, item = 0, u = 0;
+      const bool ok = for_items([&](int, int, int, int t0, int t1) {
+        for (int t = t0; t < t1; ++t, ++u) {
+          if (!mbar_wait<false>(smem_u32(&ctl.acc_empty[u & 1]), ((u >> 1) & 1) ^ 1, abort, timeout_ns)) return false;
+          const uint32_t d = tmem + (u & 1) * kAccCols;
+#pragma unroll 1
+          for (int j = 0; j < kChunks; ++j) {
+            const bool rope = j == kChunks - 1;
+            const int qj = kFp8 ? (rope ? kQChunks - 1 : 0) : j;   // the barrier of this chunk's query
+            if (t == t0 && !mbar_wait<false>(smem_u32(&ctl.q_full[qj]), item & 1, abort, timeout_ns)) return false;
+            if (!mbar_wait<false>(smem_u32(&ctl.full[slot]), phase, abort, timeout_ns)) return false;
+            tc_fence_after();
+            const uint32_t ka = sRing + slot * kSlot;
+            if (kFp8 && !rope) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                // 32 codes = 32 bytes of every 128-byte row; hi then lo into the same accumulator
+                const uint64_t ad = smem_desc(ka + kk * 32, 16, 1024, kSwizzle128B);
+                mma_f8_ss(d, ad, smem_desc(sQ + j * q_chunk + kk * 32, 16, 1024, kSwizzle128B), idesc8, (j | kk) ? 1u : 0u);
+                mma_f8_ss(d, ad, smem_desc(sQ + (4 + j) * q_chunk + kk * 32, 16, 1024, kSwizzle128B), idesc8, 1u);
+              }
+            } else {
+              const uint32_t qb = sQ + (rope ? kQChunks - 1 : j) * q_chunk;
+              const uint32_t dd = kFp8 ? d + kGroupRows : d;   // e4m3: RoPE scores in their own columns
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ss(dd, smem_desc(ka + kk * 32, 16, 1024, kSwizzle128B), smem_desc(qb + kk * 32, 16, 1024, kSwizzle128B),
+                       idesc16, (kFp8 ? kk : j | kk) ? 1u : 0u);
+            }
+            mma_commit(smem_u32(&ctl.empty[slot]));
+            if (t == t1 - 1 && (!kFp8 || rope)) {   // the query's chunk is free (e4m3: all of it) for the next item
+              mma_commit(smem_u32(&ctl.q_empty[rope ? kQChunks - 1 : j]));
+              if (kFp8) mma_commit(smem_u32(&ctl.q_empty[0]));
+            }
+            if (++slot == slots) {
+              slot = 0;
+              phase ^= 1;
+            }
+          }
+          mma_commit(smem_u32(&ctl.acc_full[u & 1]));
+        }
+        ++item;
+        return true;
+      });
+      int dummy = 0;
+      mma_commit(smem_u32(&ctl.drain));
+      mbar_wait<false>(smem_u32(&ctl.drain), 0, &dummy, drain_ns);
+      if (!ok) set_status(a.status, MLA_ERR_TIMEOUT);
+    }
+  } else if (warp >= kSplitWarp) {
+    // ---------------------------------------------------------------- e4m3: the query in two terms
+    if constexpr (kFp8) {
+      uint32_t item = 0;
+      const bool ok = for_items([&](int b, int, int g, int, int) {
+        if (!__all_sync(0xffffffffu, mbar_wait<false>(smem_u32(&ctl.q_empty[0]), (item & 1) ^ 1, abort, timeout_ns)))
+          return false;
+        constexpr int kU = 4;   // rows in flight per warp
+        for (int r0 = kU * (warp - kSplitWarp); r0 < N; r0 += 4 * kU) {
+          uint4 v[kU][2];
+#pragma unroll
+          for (int i = 0; i < kU; ++i) {
+            const int row = g * kGroupRows + r0 + i;
+            const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)a.q_lat +
+                                                             ((size_t)b * a.rows + row) * kR) + 2 * lane;
+            v[i][0] = row < a.rows ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
+            v[i][1] = row < a.rows ? __ldg(src + 1) : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+          for (int i = 0; i < kU; ++i) {
+            const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+            uint32_t hi[4], lo[4];
+            const uint32_t up = split_row(w, hi, lo);
+            const int r = r0 + i;
+            // lane's 16 channels: 16-byte piece lane % 8 of the row in chunk lane / 8, 128-byte swizzle
+            uint8_t* dst = gQ + (lane >> 3) * q_chunk + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dst + 4 * q_chunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (lane == 0) ctl.pow2[r] = (uint8_t)up;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.q_full[0]));
+        ++item;
+        return true;
+      });
+      if (!ok) set_status(a.status, MLA_ERR_TIMEOUT);
+    }
+  } else {
+    // ---------------------------------------------------------------- sums (thread = token)
+    const int tr = threadIdx.x;   // TMEM lane
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const float qnan = __uint_as_float(0x7FC00000u);
+    uint32_t item = 0, u = 0;
+    bool ok = true;
+    for_items([&](int b, int Lc, int g, int t0, int t1) {
+      // the group's rows (all four warps are done with the previous item's)
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      {
+        const int row = g * kGroupRows + tr;
+        const bool valid = row < a.rows && tr < N;
+        const size_t qrow = (size_t)b * a.rows + row;
+        ctl.l2[tr] = valid ? __ldg(m.lse + qrow) * kLog2e : INFINITY;
+      }
+      if constexpr (kFp8) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait<false>(smem_u32(&ctl.q_full[0]), item & 1, abort, timeout_ns));
+        ctl.a2[tr] = tr < N ? __uint_as_float((uint32_t)ctl.pow2[tr] << 23) * a.scale_log2 : 0.f;
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (kFp8 && tr == 0) mbar_arrive(smem_u32(&ctl.q_empty[0]));
+      const int least = a.causal ? Lc - a.Sq + 1 : Lc;   // tokens before this one are seen by every row
+      for (int t = t0; t < t1; ++t, ++u) {
+        const int tok = t * kTile + tr;
+        const bool mine = tok < Lc;
+        float* out = m.mass + (size_t)b * m.max_seq_len + tok;
+        float before = 0.f, ks = 0.f;
+        bool good = true;
+        if (mine) {
+          const int blk = __ldg(a.block_table + (size_t)b * a.max_blocks + tok / kBS);
+          good = blk >= 0 && blk < a.num_blocks;
+          if (!good) set_status(a.status, MLA_ERR_BAD_BLOCK_ID);
+          if (kFp8 && good) ks = __ldg(a.kv_scale + (size_t)blk * kBS + tok % kBS);
+          // group 0 starts from mass_in, the others from what this thread stored for the group before
+          if (g > 0)
+            before = *out;
+          else if (m.mass_in)
+            before = m.mass_in[(size_t)b * m.max_seq_len + tok];
+        }
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait<false>(smem_u32(&ctl.acc_full[u & 1]), (u >> 1) & 1, abort, timeout_ns));
+        if (!ok) {   // a wait ran out: the tokens left become NaN
+          if (mine) *out = qnan;
+          continue;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + lane_off + (u & 1) * kAccCols;
+        const bool all = (t + 1) * kTile <= least;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < N; c += 16) {
+          uint32_t v[16], r[16];
+          tmem_ld16(d + c, v);
+          if constexpr (kFp8) tmem_ld16(d + kGroupRows + c, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            float x[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int k = c + i + e;
+              if constexpr (kFp8)
+                x[e] = fmaf(__uint_as_float(v[i + e]) * ks, ctl.a2[k], fmaf(__uint_as_float(r[i + e]), a.scale_log2, -ctl.l2[k]));
+              else
+                x[e] = fmaf(__uint_as_float(v[i + e]), a.scale_log2, -ctl.l2[k]);
+              // (a causal row sees one token more than the row of the query token before)
+              if (!all && tok >= least + (a.causal ? (g * kGroupRows + k) / a.H : 0)) x[e] = -INFINITY;
+            }
+            s0 += ex2_approx(x[0]);
+            s1 += ex2_approx(x[1]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.acc_empty[u & 1]));
+        if (mine) *out = good ? before + (s0 + s1) : qnan;
+      }
+      ++item;
+      return true;
+    });
+    if (!ok) set_status(a.status, MLA_ERR_TIMEOUT);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------- host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = (EncodeTiledFn)p;
+  });
+  return fn;
+}
+
+// [d2][d1][d0] elements of `size` bytes, contiguous; boxes of 128 bytes x `rows`, 128-byte swizzle
+bool map_rows(CUtensorMap* tm, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, int size, uint32_t rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {d0 * size, d0 * d1 * size};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / size), rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(tm, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
-bool mass_tc_supported(int, int, int, int, int) { return false; }
-cudaError_t launch_mass_tc(const MassArgs&, cudaStream_t) { return cudaErrorInvalidValue; }
+bool mass_tc_supported(int r, int d_r, int block_size, int q_dtype, int cache_dtype) {
+  return r == kR && d_r == kDR && block_size == kBS && q_dtype == kBF16 && (cache_dtype == kBF16 || cache_dtype == kE4M3);
+}
+
+cudaError_t launch_mass_tc(const MassArgs& m0, cudaStream_t s) {
+  MassArgs m = m0;
+  const DecodeArgs& a = m.d;
+  const bool fp8 = a.cache_dtype == kE4M3;
+  // MMA N: the rows of a group, in steps of 16
+  const int N = std::min(kGroupRows, (a.rows + 15) / 16 * 16);
+  const uint32_t q_bytes = kQChunks * (uint32_t)N * 128;
+  const int slots = (int)std::min<uint32_t>(kMaxSlots, (kSmemMax - 1024 - kCtlBytes - q_bytes) / kSlot);
+  const uint32_t smem = 1024 + kCtlBytes + q_bytes + (uint32_t)slots * kSlot;
+  CUtensorMap tq, tqr, tkv, tkr;
+  if (!map_rows(&tq, a.q_lat, kR, a.rows, a.B, 2, N) || !map_rows(&tqr, a.q_rope, kDR, a.rows, a.B, 2, N) ||
+      !(fp8 ? map_rows(&tkv, a.cache, kR, kBS, a.num_blocks, 1, kBS) && map_rows(&tkr, a.k_rope, kDR, kBS, a.num_blocks, 2, kBS)
+            : map_rows(&tkv, a.cache, kR + kDR, kBS, a.num_blocks, 2, kBS)))
+    return cudaErrorInvalidValue;
+  if (!fp8) tkr = tkv;   // unused
+  auto kernel = fp8 ? mass_tc_kernel<true> : mass_tc_kernel<false>;
+  static std::once_flag once[2][64];
+  static int sms[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t err = cudaSuccess;
+  std::call_once(once[fp8 ? 1 : 0][dev & 63], [&] {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms[dev & 63], cudaDevAttrMultiProcessorCount, dev);
+  });
+  if (err != cudaSuccess) return err;
+  // one CTA per SM, fewer when there cannot be as many tiles
+  const long long most = (long long)a.B * ((a.len_cap + kTile - 1) / kTile);
+  if (m.d.W == 0) m.d.W = (int)std::min<long long>(std::max(sms[dev & 63], 1), std::max(most, 1ll));
+  kernel<<<m.d.W, kTcThreads, smem, s>>>(tq, tqr, tkv, tkr, m, N, slots, wait_timeout_ns(), drain_timeout_ns());
+  return cudaGetLastError();
+}
 
 cudaError_t launch_mass_simt(const MassArgs& m, cudaStream_t s) {
   const int smem = kTok * (m.d.r + m.d.d_r + 1) * (int)sizeof(float);
