@@ -124,8 +124,9 @@ constexpr int kMaxSlots = 12;
 constexpr int kQChunks = 9;                      // query: 9 x [N rows][128 bytes]
 constexpr int kGroupRows = 128;                  // query rows per group (at most)
 constexpr int kGroupRun = 4;                     // tiles per run when there are several groups
-constexpr int kTcThreads = 320;                  // warps 0-3 sums, 4 TMA, 5 MMA, 6-9 query split (e4m3)
-constexpr int kTmaWarp = 4, kMmaWarp = 5, kSplitWarp = 6;
+// warps 0-7 sums (0-3 the even tiles, 4-7 the odd ones), 8 TMA, 9 MMA, 10-13 query split (e4m3)
+constexpr int kSumThreads = 256, kTmaWarp = 8, kMmaWarp = 9, kSplitWarp = 10;
+constexpr int kTcThreads = 32 * 14;
 constexpr uint32_t kCtlBytes = 2048;             // leaves 5 ring slots at 128 rows
 constexpr uint32_t kSmemMax = 232448;
 
@@ -137,8 +138,9 @@ struct MassCtl {
   uint32_t tmem_base;
   int abort;
   WorkerPlan plan;
-  float l2[kGroupRows];      // lse * log2(e) of the group's rows; +inf for rows that are none
-  float a2[kGroupRows];      // e4m3: the row's power of two * scale * log2(e)
+  alignas(16) float nl2[kGroupRows];   // -lse * log2(e) of the group's rows; -inf for rows that are none
+  alignas(16) float a2[kGroupRows];    // e4m3: the row's power of two * scale * log2(e)
+  uint8_t late[kGroupRows];  // causal: query tokens between the group's first row and this one
   uint8_t pow2[kGroupRows];  // e4m3: exponent field of the row's power of two (split warps -> sum warps)
 };
 static_assert(sizeof(MassCtl) <= kCtlBytes, "control block");
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctl.acc_full[i]), 1);
-      mbar_init(smem_u32(&ctl.acc_empty[i]), 4);   // one arrival per sum warp
+      mbar_init(smem_u32(&ctl.acc_empty[i]), 4);   // one arrival per sum warp of the tile
     }
     mbar_init(smem_u32(&ctl.drain), 1);
     ctl.abort = 0;
@@ -268,13 +270,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int slot = 0, issued = 0;
       uint32_t phase = 0, item = 0, q_issued = 0;   // query chunks loaded so far
       const bool ok = for_items([&](int b, int Lc, int g, int t0, int t1) {
+        const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
+        const int blocks = tiles_of(Lc, kBS);
+        int next[2] = {__ldg(bt + 2 * t0), 2 * t0 + 1 < blocks ? __ldg(bt + 2 * t0 + 1) : 0};
         for (int t = t0; t < t1; ++t) {
           int blk[2];
-          const int nblk = min(tiles_of(Lc, kBS) - 2 * t, 2);
+          const int nblk = min(blocks - 2 * t, 2);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            blk[h] = h < nblk ? __ldg(a.block_table + (size_t)b * a.max_blocks + 2 * t + h) : 0;
+            blk[h] = next[h];
             if (blk[h] < 0 || blk[h] >= a.num_blocks) blk[h] = a.num_blocks;   // past the cache: reads zeros
+            const int ahead = 2 * (t + 1) + h;   // the next tile's ids, a tile's time early
+            next[h] = t + 1 < t1 && ahead < blocks ? __ldg(bt + ahead) : 0;
           }
 #pragma unroll 1
           for (int j = 0; j < kChunks; ++j) {
@@ -417,28 +424,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- sums (thread = token)
-    const int tr = threadIdx.x;   // TMEM lane
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    // Two sets of four warps take the tiles of even and odd number, so that one set's TMEM loads and
+    // exponentials overlap the other's; a token is always one thread's.
+    const int tr = threadIdx.x & 127, set = threadIdx.x >> 7;   // tr: TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const float qnan = __uint_as_float(0x7FC00000u);
+    const unsigned long long scale2 = f2_pack(a.scale_log2, a.scale_log2);
     uint32_t item = 0, u = 0;
     bool ok = true;
     for_items([&](int b, int Lc, int g, int t0, int t1) {
-      // the group's rows (all four warps are done with the previous item's)
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      {
+      const int s_first = g * kGroupRows / a.H;   // query token of the group's first row
+      // the group's rows (all sum warps are done with the previous item's)
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (kFp8 && ok)
+        ok = __all_sync(0xffffffffu, mbar_wait<false>(smem_u32(&ctl.q_full[0]), item & 1, abort, timeout_ns));
+      if (set == 0) {
         const int row = g * kGroupRows + tr;
         const bool valid = row < a.rows && tr < N;
-        const size_t qrow = (size_t)b * a.rows + row;
-        ctl.l2[tr] = valid ? __ldg(m.lse + qrow) * kLog2e : INFINITY;
+        ctl.nl2[tr] = valid ? -__ldg(m.lse + (size_t)b * a.rows + row) * kLog2e : -INFINITY;
+        ctl.late[tr] = valid ? (uint8_t)(row / a.H - s_first) : 0;
+        if constexpr (kFp8)
+          ctl.a2[tr] = tr < N ? __uint_as_float((uint32_t)ctl.pow2[tr] << 23) * a.scale_log2 : 0.f;
       }
-      if constexpr (kFp8) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait<false>(smem_u32(&ctl.q_full[0]), item & 1, abort, timeout_ns));
-        ctl.a2[tr] = tr < N ? __uint_as_float((uint32_t)ctl.pow2[tr] << 23) * a.scale_log2 : 0.f;
-      }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (kFp8 && tr == 0) mbar_arrive(smem_u32(&ctl.q_empty[0]));
-      const int least = a.causal ? Lc - a.Sq + 1 : Lc;   // tokens before this one are seen by every row
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (kFp8 && threadIdx.x == 0) mbar_arrive(smem_u32(&ctl.q_empty[0]));
+      const int least = Lc - a.Sq + 1 + s_first;   // causal: every row of the group sees the tokens before this one
       for (int t = t0; t < t1; ++t, ++u) {
+        if ((t & 1) != set) continue;
         const int tok = t * kTile + tr;
         const bool mine = tok < Lc;
         float* out = m.mass + (size_t)b * m.max_seq_len + tok;
@@ -462,35 +474,62 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + lane_off + (u & 1) * kAccCols;
-        const bool all = (t + 1) * kTile <= least;
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll 1
-        for (int c = 0; c < N; c += 16) {
-          uint32_t v[16], r[16];
-          tmem_ld16(d + c, v);
-          if constexpr (kFp8) tmem_ld16(d + kGroupRows + c, r);
-          tmem_wait_ld();
+        const bool masked = a.causal && (t + 1) * kTile > least;   // (tokens past the length are not stored)
+        const unsigned long long ks2 = f2_pack(ks, ks);
+        unsigned long long sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+        // 16 columns (rows) at a time, the next 16 on their way out of TMEM meanwhile
+        uint32_t v[2][16], r[2][16];
+        auto fetch = [&](int c, int k) {
+          tmem_ld16(d + c, v[k]);
+          if constexpr (kFp8) tmem_ld16(d + kGroupRows + c, r[k]);
+        };
+        auto add = [&](int c, int k) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            float x[2];
+          for (int i = 0; i < 16; i += 4) {
+            const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(&ctl.nl2[c + i]);
+            ulonglong2 ar = make_ulonglong2(0ull, 0ull);
+            if constexpr (kFp8) ar = *reinterpret_cast<const ulonglong2*>(&ctl.a2[c + i]);
+            const uint32_t late = *reinterpret_cast<const uint32_t*>(&ctl.late[c + i]);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int k = c + i + e;
-              if constexpr (kFp8)
-                x[e] = fmaf(__uint_as_float(v[i + e]) * ks, ctl.a2[k], fmaf(__uint_as_float(r[i + e]), a.scale_log2, -ctl.l2[k]));
-              else
-                x[e] = fmaf(__uint_as_float(v[i + e]), a.scale_log2, -ctl.l2[k]);
-              // (a causal row sees one token more than the row of the query token before)
-              if (!all && tok >= least + (a.causal ? (g * kGroupRows + k) / a.H : 0)) x[e] = -INFINITY;
+            for (int h = 0; h < 2; ++h) {
+              const int e = i + 2 * h;
+              const unsigned long long vv = f2_pack(__uint_as_float(v[k][e]), __uint_as_float(v[k][e + 1]));
+              unsigned long long x;
+              if constexpr (kFp8) {
+                const unsigned long long rr = f2_pack(__uint_as_float(r[k][e]), __uint_as_float(r[k][e + 1]));
+                x = fma2(mul2(vv, ks2), h ? ar.y : ar.x, fma2(rr, scale2, h ? nl.y : nl.x));
+              } else {
+                x = fma2(vv, scale2, h ? nl.y : nl.x);
+              }
+              float x0, x1;
+              f2_unpack(x, x0, x1);
+              if (masked) {
+                if (tok >= least + (int)((late >> (16 * h)) & 255u)) x0 = -INFINITY;
+                if (tok >= least + (int)((late >> (16 * h + 8)) & 255u)) x1 = -INFINITY;
+              }
+              sum[h] = add2(sum[h], f2_pack(ex2_approx(x0), ex2_approx(x1)));
             }
-            s0 += ex2_approx(x[0]);
-            s1 += ex2_approx(x[1]);
           }
+        };
+        fetch(0, 0);
+        tmem_wait_ld();
+#pragma unroll 1
+        for (int c = 0; c < N; c += 32) {   // N is a multiple of 16
+          if (c + 16 < N) fetch(c + 16, 1);
+          add(c, 0);
+          tmem_wait_ld();
+          if (c + 16 >= N) break;
+          if (c + 32 < N) fetch(c + 32, 0);
+          add(c + 16, 1);
+          tmem_wait_ld();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl.acc_empty[u & 1]));
-        if (mine) *out = good ? before + (s0 + s1) : qnan;
+        float p0, p1, p2, p3;
+        f2_unpack(sum[0], p0, p1);
+        f2_unpack(sum[1], p2, p3);
+        if (mine) *out = good ? before + ((p0 + p1) + (p2 + p3)) : qnan;
       }
       ++item;
       return true;
