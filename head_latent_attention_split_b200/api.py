@@ -166,43 +166,42 @@ def sparse_decode(q_lat, q_rope, kv_cache, block_table, indices, counts, softmax
 #
 # The calls below check their tensors (device, type, shape, contiguity) before the library sees a
 # pointer, run on the tensors' device whatever the current one is, and allocate on the stream
-# they launch on.
-class _On:
-    """Context of one call: `dev` is current inside it, and `stream` (a torch stream, a raw handle
-    or None for the current one)."""
-    __slots__ = ("ctx",)
-
-    def __init__(self, dev, stream):
-        import torch
-        self.ctx = None
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
-            if stream.device != dev:
-                raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
-            self.ctx = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != dev.index:
-            self.ctx = torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+# they launch on. A small call's kernels take a few microseconds, so the checks are one expression
+# per tensor, the argument structures are filled by position, and new tensors come from empty_like and
+# empty_strided (1.3 and 1.4 us a call where torch.empty takes 2.2).
+def _raw_stream(dev):
+    """Handle of dev's current stream."""
+    import torch
+    try:
+        return torch._C._cuda_getCurrentRawStream(dev.index)   # torch.cuda.current_stream without the object
+    except AttributeError:
+        return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _need(dev, what, t, dtypes, shape):
-    """t is a contiguous tensor on dev of one of `dtypes` and of `shape`."""
+def _away(dev, stream):
+    """None when the call can run as it stands (on dev's current stream, dev current), else a context that
+    makes dev and `stream` (a torch stream or a raw handle) current."""
+    import torch
+    if stream is None:
+        return None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _need(dev, what, t, dtype, shape):
+    """t is a contiguous tensor on dev of `dtype` and `shape`."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return
     if t.device != dev:
         raise ValueError(f"{what} is on {t.device}, expected {dev}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{what}: unsupported dtype {t.dtype}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    raise ValueError(f"{what} must be contiguous")
 
 
 def _cuda_device(t, what):
@@ -212,38 +211,48 @@ def _cuda_device(t, what):
 
 
 def _dims(t, what, n):
-    if t.dim() != n:
-        raise ValueError(f"{what} must have {n} dimensions, got {t.dim()}")
-    return t.shape
+    s = t.shape
+    if len(s) != n:
+        raise ValueError(f"{what} must have {n} dimensions, got {len(s)}")
+    return s
 
 
-def _check_step(q_lat, q_rope, kv_cache, block_table, seq_lens, k_rope_cache, kv_scale):
-    """The tensors of a decode step fit one another; returns their device."""
+def _step(q_lat, q_rope, kv_cache, block_table, seq_lens, softmax_scale, causal, k_rope_cache, kv_scale, out_dtype,
+          num_workers, kernel):
+    """Checks that the tensors of a decode step fit one another; their device and parameters."""
     import torch
     dev = _cuda_device(q_lat, "q_lat")
     B, Sq, H, r = _dims(q_lat, "q_lat", 4)
     d_r = 0 if q_rope is None else _dims(q_rope, "q_rope", 4)[3]
-    nb, bs, width = _dims(kv_cache, "kv_cache", 3)
-    f32, bf16, i32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
-    fp8 = kv_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
-    qt = bf16 if fp8 else (kv_cache.dtype,)
+    nb, bs, _ = _dims(kv_cache, "kv_cache", 3)
+    mb = _dims(block_table, "block_table", 2)[1]
+    ct = kv_cache.dtype
+    cd = _dtype_code(kv_cache, "kv_cache")
+    qt = torch.bfloat16 if cd == _b.E4M3 else ct
     _need(dev, "q_lat", q_lat, qt, (B, Sq, H, r))
     if q_rope is not None:
         _need(dev, "q_rope", q_rope, qt, (B, Sq, H, d_r))
-    if fp8:
-        _need(dev, "kv_cache", kv_cache, (kv_cache.dtype,), (nb, bs, r))
+    if cd == _b.E4M3:
+        _need(dev, "kv_cache", kv_cache, ct, (nb, bs, r))
         if kv_scale is None or (d_r > 0 and k_rope_cache is None):
             raise ValueError("an e4m3 cache needs k_rope_cache and kv_scale")
         if k_rope_cache is not None:
-            _need(dev, "k_rope_cache", k_rope_cache, bf16, (nb, bs, d_r))
-        _need(dev, "kv_scale", kv_scale, f32, (nb, bs))
+            _need(dev, "k_rope_cache", k_rope_cache, torch.bfloat16, (nb, bs, d_r))
+        _need(dev, "kv_scale", kv_scale, torch.float32, (nb, bs))
     else:
-        _need(dev, "kv_cache", kv_cache, f32 + bf16, (nb, bs, r + d_r))
+        _need(dev, "kv_cache", kv_cache, ct, (nb, bs, r + d_r))
         if k_rope_cache is not None or kv_scale is not None:
             raise ValueError("k_rope_cache and kv_scale belong to an e4m3 cache")
-    _need(dev, "block_table", block_table, i32, (B, _dims(block_table, "block_table", 2)[1]))
-    _need(dev, "seq_lens", seq_lens, i32, (B,))
-    return dev
+    _need(dev, "block_table", block_table, torch.int32, (B, mb))
+    _need(dev, "seq_lens", seq_lens, torch.int32, (B,))
+    qd = _b.BF16 if cd == _b.E4M3 else cd
+    if out_dtype is None:
+        out_dtype = qd
+    return dev, _b.Params(B, Sq, H, r, d_r, bs, nb, mb, qd, cd, out_dtype, 1 if causal else 0, softmax_scale, num_workers,
+                          _b.KERNELS[kernel] if isinstance(kernel, str) else kernel, 0)
+
+
+_workspace_bytes = {}   # (device, parameters) -> mla_decode_workspace_size, a function of nothing else
 
 
 def window_decode(q_lat, q_rope, kv_cache, block_table, seq_lens, softmax_scale, window, sinks=0, causal=False,
@@ -255,24 +264,36 @@ def window_decode(q_lat, q_rope, kv_cache, block_table, seq_lens, softmax_scale,
     Other arguments and the returned (out, lse) are decode's.
     """
     import torch
-    dev = _check_step(q_lat, q_rope, kv_cache, block_table, seq_lens, k_rope_cache, kv_scale)
-    p = params_for(q_lat, q_rope, kv_cache, block_table, softmax_scale, causal, out_dtype, num_workers, kernel)
-    if p.out_dtype not in (_b.F32, _b.BF16):
-        raise TypeError("out_dtype must be F32 or BF16")
+    dev, p = _step(q_lat, q_rope, kv_cache, block_table, seq_lens, softmax_scale, causal, k_rope_cache, kv_scale,
+                   out_dtype, num_workers, kernel)
+    away = _away(dev, stream)
+    if away is not None:
+        with away:
+            return window_decode(q_lat, q_rope, kv_cache, block_table, seq_lens, softmax_scale, window, sinks, causal,
+                                 k_rope_cache, kv_scale, out, lse, workspace, out_dtype, num_workers, kernel)
+    shape = q_lat.shape
+    B, Sq, H, _ = shape
     od = torch.float32 if p.out_dtype == _b.F32 else torch.bfloat16
-    with _On(dev, stream):
-        if out is None:
-            out = torch.empty(q_lat.shape, dtype=od, device=dev)
-        else:
-            _need(dev, "out", out, (od,), q_lat.shape)
-        if lse is None:
-            lse = torch.empty(q_lat.shape[:3], dtype=torch.float32, device=dev)
-        else:
-            _need(dev, "lse", lse, (torch.float32,), q_lat.shape[:3])
-        if workspace is None:
-            workspace = torch.empty(max(_b.workspace_size(p), 1), dtype=torch.uint8, device=dev)
-        _b.mla_window_decode(p, window, sinks, q_lat, q_rope, kv_cache, k_rope_cache, kv_scale, block_table, seq_lens,
-                             out, lse, workspace)
+    if out is None:
+        out = torch.empty_like(q_lat, dtype=od)
+    else:
+        _need(dev, "out", out, od, shape)
+    if lse is None:
+        lse = torch.empty_strided((B, Sq, H), (Sq * H, H, 1), dtype=torch.float32, device=dev)
+    else:
+        _need(dev, "lse", lse, torch.float32, shape[:3])
+    if workspace is None:
+        key = (dev.index, bytes(p))
+        n = _workspace_bytes.get(key)
+        if n is None:
+            if len(_workspace_bytes) >= 4096:
+                _workspace_bytes.clear()
+            n = _workspace_bytes[key] = max(_b.workspace_size(p), 1)
+        workspace = torch.empty_strided((n,), (1,), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of q_lat")
+    _b.mla_window_decode(p, window, sinks, q_lat, q_rope, kv_cache, k_rope_cache, kv_scale, block_table, seq_lens, out, lse,
+                         workspace, stream=_raw_stream(dev))
     return out, lse
 
 
@@ -286,17 +307,22 @@ def attention_mass(q_lat, q_rope, kv_cache, block_table, seq_lens, lse, softmax_
     Returns mass.
     """
     import torch
-    dev = _check_step(q_lat, q_rope, kv_cache, block_table, seq_lens, k_rope_cache, kv_scale)
-    f32 = (torch.float32,)
-    _need(dev, "lse", lse, f32, q_lat.shape[:3])
+    dev, p = _step(q_lat, q_rope, kv_cache, block_table, seq_lens, softmax_scale, causal, k_rope_cache, kv_scale, None,
+                   num_workers, kernel)
+    shape = q_lat.shape
+    _need(dev, "lse", lse, torch.float32, shape[:3])
     S = _dims(mass, "mass", 2)[1]
-    _need(dev, "mass", mass, f32, (q_lat.shape[0], S))
+    _need(dev, "mass", mass, torch.float32, (shape[0], S))
     if mass_in is not None and mass_in is not mass:
-        _need(dev, "mass_in", mass_in, f32, mass.shape)
-    p = params_for(q_lat, q_rope, kv_cache, block_table, softmax_scale, causal, None, num_workers, kernel)
-    with _On(dev, stream):
-        _b.mla_attention_mass(p, S, q_lat, q_rope, kv_cache, k_rope_cache, kv_scale, block_table, seq_lens, lse,
-                              mass_in, mass)
+        _need(dev, "mass_in", mass_in, torch.float32, (shape[0], S))
+    away = _away(dev, stream)
+    if away is not None:
+        with away:
+            _b.mla_attention_mass(p, S, q_lat, q_rope, kv_cache, k_rope_cache, kv_scale, block_table, seq_lens, lse,
+                                  mass_in, mass)
+        return mass
+    _b.mla_attention_mass(p, S, q_lat, q_rope, kv_cache, k_rope_cache, kv_scale, block_table, seq_lens, lse, mass_in, mass,
+                          stream=_raw_stream(dev))
     return mass
 
 
@@ -307,19 +333,23 @@ def evict_select(mass, seq_lens, budget, sinks=0, recent=0, indices=None, counts
     import torch
     dev = _cuda_device(mass, "mass")
     B, S = _dims(mass, "mass", 2)
-    i32 = (torch.int32,)
-    _need(dev, "mass", mass, (torch.float32,), (B, S))
+    i32 = torch.int32
+    _need(dev, "mass", mass, torch.float32, (B, S))
     _need(dev, "seq_lens", seq_lens, i32, (B,))
-    with _On(dev, stream):
-        if indices is None:
-            indices = torch.empty((B, max(budget, 0)), dtype=torch.int32, device=dev)
-        else:
-            _need(dev, "indices", indices, i32, (B, budget))
-        if counts is None:
-            counts = torch.empty((B,), dtype=torch.int32, device=dev)
-        else:
-            _need(dev, "counts", counts, i32, (B,))
-        _b.mla_evict_select(_b.EvictParams(B, S, budget, sinks, recent, 0), mass, seq_lens, indices, counts)
+    if indices is not None:
+        _need(dev, "indices", indices, i32, (B, budget))
+    if counts is not None:
+        _need(dev, "counts", counts, i32, (B,))
+    away = _away(dev, stream)
+    if away is not None:
+        with away:
+            return evict_select(mass, seq_lens, budget, sinks, recent, indices, counts)
+    if indices is None:
+        indices = torch.empty_strided((B, max(budget, 0)), (max(budget, 1), 1), dtype=i32, device=dev)
+    if counts is None:
+        counts = torch.empty_like(seq_lens)
+    _b.mla_evict_select(_b.EvictParams(B, S, budget, sinks, recent, 0), mass, seq_lens, indices, counts,
+                        stream=_raw_stream(dev))
     return indices, counts
 
 
@@ -332,28 +362,35 @@ def cache_compact(kv_cache, block_table, dst_block_table, indices, counts, k_rop
     dev = _cuda_device(kv_cache, "kv_cache")
     nb, bs, width = _dims(kv_cache, "kv_cache", 3)
     B, k = _dims(indices, "indices", 2)
-    i32, f32 = (torch.int32,), (torch.float32,)
-    _need(dev, "kv_cache", kv_cache, (torch.float32, torch.bfloat16, torch.uint8, torch.float8_e4m3fn), kv_cache.shape)
-    _need(dev, "block_table", block_table, i32, (B, _dims(block_table, "block_table", 2)[1]))
-    _need(dev, "dst_block_table", dst_block_table, i32, (B, _dims(dst_block_table, "dst_block_table", 2)[1]))
+    i32, f32 = torch.int32, torch.float32
+    cd = _dtype_code(kv_cache, "kv_cache")
+    mb, db = _dims(block_table, "block_table", 2)[1], _dims(dst_block_table, "dst_block_table", 2)[1]
+    _need(dev, "kv_cache", kv_cache, kv_cache.dtype, (nb, bs, width))
+    _need(dev, "block_table", block_table, i32, (B, mb))
+    _need(dev, "dst_block_table", dst_block_table, i32, (B, db))
     _need(dev, "indices", indices, i32, (B, k))
     _need(dev, "counts", counts, i32, (B,))
-    d_r = 0
+    d_r = ms = mo = 0
     if k_rope_cache is not None:
         d_r = _dims(k_rope_cache, "k_rope_cache", 3)[2]
-        _need(dev, "k_rope_cache", k_rope_cache, (torch.bfloat16,), (nb, bs, d_r))
+        _need(dev, "k_rope_cache", k_rope_cache, torch.bfloat16, (nb, bs, d_r))
     if kv_scale is not None:
         _need(dev, "kv_scale", kv_scale, f32, (nb, bs))
     if mass is not None:
-        _need(dev, "mass", mass, f32, (B, _dims(mass, "mass", 2)[1]))
+        ms = _dims(mass, "mass", 2)[1]
+        _need(dev, "mass", mass, f32, (B, ms))
     if mass_out is not None:
-        _need(dev, "mass_out", mass_out, f32, (B, _dims(mass_out, "mass_out", 2)[1]))
-    p = _b.CompactParams(B, width, d_r, bs, nb, block_table.shape[1], dst_block_table.shape[1],
-                         _dtype_code(kv_cache, "kv_cache"), k, 0 if mass is None else mass.shape[1],
-                         0 if mass_out is None else mass_out.shape[1], 0)
-    with _On(dev, stream):
-        _b.mla_cache_compact(p, kv_cache, k_rope_cache, kv_scale, block_table, dst_block_table, indices, counts, mass,
-                             mass_out)
+        mo = _dims(mass_out, "mass_out", 2)[1]
+        _need(dev, "mass_out", mass_out, f32, (B, mo))
+    p = _b.CompactParams(B, width, d_r, bs, nb, mb, db, cd, k, ms, mo, 0)
+    away = _away(dev, stream)
+    if away is not None:
+        with away:
+            _b.mla_cache_compact(p, kv_cache, k_rope_cache, kv_scale, block_table, dst_block_table, indices, counts, mass,
+                                 mass_out)
+        return
+    _b.mla_cache_compact(p, kv_cache, k_rope_cache, kv_scale, block_table, dst_block_table, indices, counts, mass, mass_out,
+                         stream=_raw_stream(dev))
 
 
 def verify_drafts(target_probs, draft_probs, draft_tokens, accept_u, sample_u, draft_lens=None, seq_lens=None,
@@ -371,29 +408,37 @@ def verify_drafts(target_probs, draft_probs, draft_tokens, accept_u, sample_u, d
     dev = _cuda_device(target_probs, "target_probs")
     B, K1, V = _dims(target_probs, "target_probs", 3)
     K = K1 - 1
-    pt, i32, f32 = (torch.float32, torch.bfloat16), (torch.int32,), (torch.float32,)
-    _need(dev, "target_probs", target_probs, pt, target_probs.shape)
+    pt, i32 = target_probs.dtype, torch.int32
+    pd = _b.F32 if pt is torch.float32 else _b.BF16
+    _need(dev, "target_probs", target_probs, pt if pt is torch.float32 else torch.bfloat16, (B, K1, V))
     if draft_probs is not None:
-        _need(dev, "draft_probs", draft_probs, (target_probs.dtype,), (B, K, V))
+        _need(dev, "draft_probs", draft_probs, pt, (B, K, V))
     _need(dev, "draft_tokens", draft_tokens, i32, (B, K))
-    _need(dev, "accept_u", accept_u, f32, (B, K))
-    _need(dev, "sample_u", sample_u, f32, (B,))
-    for what, t in (("draft_lens", draft_lens), ("seq_lens", seq_lens), ("accepted", accepted),
-                    ("new_seq_lens", new_seq_lens)):
-        if t is not None:
-            _need(dev, what, t, i32, (B,))
-    if new_seq_lens is not None and seq_lens is None:
+    _need(dev, "accept_u", accept_u, torch.float32, (B, K))
+    _need(dev, "sample_u", sample_u, torch.float32, (B,))
+    if draft_lens is not None:
+        _need(dev, "draft_lens", draft_lens, i32, (B,))
+    if seq_lens is not None:
+        _need(dev, "seq_lens", seq_lens, i32, (B,))
+    elif new_seq_lens is not None:
         raise ValueError("new_seq_lens needs seq_lens")
-    with _On(dev, stream):
-        if tokens is None:
-            tokens = torch.empty((B, K1), dtype=torch.int32, device=dev)
-        else:
-            _need(dev, "tokens", tokens, i32, (B, K1))
-        if accepted is None:
-            accepted = torch.empty((B,), dtype=torch.int32, device=dev)
-        if seq_lens is not None and new_seq_lens is None:
-            new_seq_lens = torch.empty((B,), dtype=torch.int32, device=dev)
-        _b.mla_verify_drafts(_b.VerifyParams(B, K, V, _dtype_code(target_probs, "target_probs"), 0), target_probs,
-                             draft_probs, draft_tokens, draft_lens, accept_u, sample_u, seq_lens, tokens, accepted,
-                             new_seq_lens)
+    if tokens is not None:
+        _need(dev, "tokens", tokens, i32, (B, K1))
+    if accepted is not None:
+        _need(dev, "accepted", accepted, i32, (B,))
+    if new_seq_lens is not None:
+        _need(dev, "new_seq_lens", new_seq_lens, i32, (B,))
+    away = _away(dev, stream)
+    if away is not None:
+        with away:
+            return verify_drafts(target_probs, draft_probs, draft_tokens, accept_u, sample_u, draft_lens, seq_lens, tokens,
+                                 accepted, new_seq_lens)
+    if tokens is None:
+        tokens = torch.empty_strided((B, K1), (K1, 1), dtype=i32, device=dev)
+    if accepted is None:
+        accepted = torch.empty_strided((B,), (1,), dtype=i32, device=dev)
+    if seq_lens is not None and new_seq_lens is None:
+        new_seq_lens = torch.empty_like(seq_lens)
+    _b.mla_verify_drafts(_b.VerifyParams(B, K, V, pd, 0), target_probs, draft_probs, draft_tokens, draft_lens, accept_u,
+                         sample_u, seq_lens, tokens, accepted, new_seq_lens, stream=_raw_stream(dev))
     return (tokens, accepted) if seq_lens is None else (tokens, accepted, new_seq_lens)

@@ -140,7 +140,10 @@ class _Lib:
     def __getattr__(self, name):
         if _Lib._handle is None:
             _Lib._handle = _load()
-        return getattr(_Lib._handle, name)
+        f = getattr(_Lib._handle, name)
+        if name in EXPORTED:
+            self.__dict__[name] = f     # found directly from now on
+        return f
 
 
 lib = _Lib()
@@ -182,10 +185,12 @@ def resolve(p: Params):
 def _addr(x):
     if x is None:
         return None
+    try:
+        return x.data_ptr()     # torch tensors first: the common case
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if isinstance(x, np.ndarray):
         return x.ctypes.data
     raise TypeError(type(x))
