@@ -11,9 +11,10 @@
 // A row of a few KB to half a MB is far from any bandwidth: the barriers and the histogram's
 // shared-memory atomics bound it.
 //
-// Compact: a copy, bound by memory: every kept row read and written once. A CTA takes 32 entries of
-// one sequence and moves their rows as one flat list of 16-byte pieces (9 per thread for a 1152-byte
-// row), so the loads of a thread do not wait for one another.
+// Compact: a copy, bound by memory: every kept row read and written once. A warp takes 8 entries of
+// one sequence: 8 lanes look their slots up, then all lanes move the 8 rows side by side in
+// 16-byte pieces, so that a lane has 8 loads in flight and the warps of an SM do not wait for one
+// another.
 #include <algorithm>
 #include <type_traits>
 
@@ -261,7 +262,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
 
 // ------------------------------------------------------------------------------ compact
 constexpr int kCpThreads = 256;
-constexpr int kCpRows = 32;   // list entries per CTA
+constexpr int kCpRows = 8;                               // list entries per warp
+constexpr int kCpSpan = kCpRows * (kCpThreads / 32);     // ... and per CTA
 
 struct CompactArgs {
   int bs, num_blocks, max_blocks, dst_blocks, list_stride, mass_stride, mass_out_stride, B;
@@ -278,66 +280,65 @@ struct CompactArgs {
   int* status;
 };
 
-// Rows src[i] -> dst[i] (i < n) of one plane, as a flat list of V-sized pieces; dst < 0: skipped.
+// One warp copies rows src[i] -> dst[i] of one plane, V-sized pieces, eight loads in flight per
+// lane; dst < 0: skipped.
 template <typename V>
-__device__ __forceinline__ void copy_rows(uint8_t* base, int row_bytes, const int* src, const int* dst, int n) {
-  const int per = row_bytes / (int)sizeof(V), total = n * per;
-  constexpr int kMlp = 9;   // loads in flight per thread
-  for (int i0 = threadIdx.x; i0 < total; i0 += kMlp * kCpThreads) {
-    V v[kMlp];
+__device__ __forceinline__ void copy_rows(uint8_t* base, int row_bytes, const int* src, const int* dst) {
+  const int per = row_bytes / (int)sizeof(V), lane = threadIdx.x & 31;
+  for (int i = lane; i < per; i += 32) {
+    V v[kCpRows];
 #pragma unroll
-    for (int u = 0; u < kMlp; ++u) {
-      const int i = i0 + u * kCpThreads;
-      if (i < total) {
-        const int r = i / per;
-        if (dst[r] >= 0) v[u] = reinterpret_cast<const V*>(base + (size_t)src[r] * row_bytes)[i - r * per];
-      }
-    }
+    for (int r = 0; r < kCpRows; ++r)
+      if (dst[r] >= 0) v[r] = reinterpret_cast<const V*>(base + (size_t)src[r] * row_bytes)[i];
 #pragma unroll
-    for (int u = 0; u < kMlp; ++u) {
-      const int i = i0 + u * kCpThreads;
-      if (i < total) {
-        const int r = i / per;
-        if (dst[r] >= 0) reinterpret_cast<V*>(base + (size_t)dst[r] * row_bytes)[i - r * per] = v[u];
-      }
-    }
+    for (int r = 0; r < kCpRows; ++r)
+      if (dst[r] >= 0) reinterpret_cast<V*>(base + (size_t)dst[r] * row_bytes)[i] = v[r];
   }
 }
 
 // kUnit: bytes per piece, dividing both planes' rows and their bases' alignment
 template <int kUnit>
 __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(const CompactArgs a) {
-  __shared__ int src[kCpRows], dst[kCpRows];
   typedef typename std::conditional<kUnit == 16, uint4, typename std::conditional<kUnit == 4, uint32_t, uint8_t>::type>::type V;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int j0 = blockIdx.x * kCpSpan + warp * kCpRows;
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
     int count = __ldg(a.counts + b);
     if (count < 0 || count > a.list_stride) {
       if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, MLA_ERR_BAD_SEQ_LEN);
       count = min(max(count, 0), a.list_stride);
     }
-    const int j0 = blockIdx.x * kCpRows, n = min(max(count - j0, 0), kCpRows);
-    if (threadIdx.x < kCpRows) {
-      const int j = j0 + threadIdx.x;
+    // lane i < 8 looks entry j0 + i up; its mass moves at once
+    const int j = j0 + lane;
+    int my_src = 0, my_dst = -1;
+    if (lane < kCpRows) {
       float m = 0.f;
       if (j < count) {
         const int t = __ldg(a.indices + (size_t)b * a.list_stride + j);
+        const int db = __ldg(a.dst_table + (size_t)b * a.dst_blocks + j / a.bs);
         const bool ok_t = t >= 0 && t < a.max_blocks * a.bs;
         const int sb = ok_t ? __ldg(a.block_table + (size_t)b * a.max_blocks + t / a.bs) : -1;
-        const int db = __ldg(a.dst_table + (size_t)b * a.dst_blocks + j / a.bs);
         const bool ok = sb >= 0 && sb < a.num_blocks && db >= 0 && db < a.num_blocks;
-        if (!ok) set_status(a.status, MLA_ERR_BAD_BLOCK_ID);
-        src[threadIdx.x] = ok ? sb * a.bs + t % a.bs : 0;
-        dst[threadIdx.x] = ok ? db * a.bs + j % a.bs : -1;
-        m = __uint_as_float(0x7FC00000u);
-        if (ok && a.mass && t < a.mass_stride) m = __ldg(a.mass + (size_t)b * a.mass_stride + t);
-        if (ok && a.kv_scale) a.kv_scale[dst[threadIdx.x]] = a.kv_scale[src[threadIdx.x]];
+        if (ok) {
+          my_src = sb * a.bs + t % a.bs;
+          my_dst = db * a.bs + j % a.bs;
+          if (a.kv_scale) a.kv_scale[my_dst] = a.kv_scale[my_src];
+        } else {
+          set_status(a.status, MLA_ERR_BAD_BLOCK_ID);
+        }
+        m = ok && a.mass && t < a.mass_stride ? __ldg(a.mass + (size_t)b * a.mass_stride + t) : __uint_as_float(0x7FC00000u);
       }
       if (a.mass && j < a.mass_out_stride) a.mass_out[(size_t)b * a.mass_out_stride + j] = m;
     }
-    __syncthreads();
-    copy_rows<V>(a.cache, a.row_bytes, src, dst, n);
-    if (a.k_rope) copy_rows<V>(a.k_rope, a.kr_bytes, src, dst, n);
-    __syncthreads();
+    if (j0 >= count) continue;
+    int src[kCpRows], dst[kCpRows];
+#pragma unroll
+    for (int r = 0; r < kCpRows; ++r) {
+      src[r] = __shfl_sync(0xffffffffu, my_src, r);
+      dst[r] = __shfl_sync(0xffffffffu, my_dst, r);
+    }
+    copy_rows<V>(a.cache, a.row_bytes, src, dst);
+    if (a.k_rope) copy_rows<V>(a.k_rope, a.kr_bytes, src, dst);
   }
 }
 
@@ -430,7 +431,7 @@ mla_status_t mla_cache_compact(const mla_compact_params_t* p, void* kv_cache, vo
     return a.row_bytes % u == 0 && aligned(a.cache, u) && (!a.k_rope || (a.kr_bytes % u == 0 && aligned(a.k_rope, u)));
   };
   const int span = mass ? p->mass_out_stride : p->list_stride;
-  const dim3 grid((unsigned)((span + kCpRows - 1) / kCpRows), (unsigned)std::min(p->batch, 65535));
+  const dim3 grid((unsigned)((span + kCpSpan - 1) / kCpSpan), (unsigned)std::min(p->batch, 65535));
   cudaStream_t s = (cudaStream_t)stream;
   if (fits(16))
     cache_compact_kernel<16><<<grid, kCpThreads, 0, s>>>(a);

@@ -16,8 +16,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kQV = kSimtMaxD / 32;   // per-lane query registers
-constexpr int kAV = kSimtMaxR / 32;   // per-lane accumulator registers
 constexpr int kChunkFloats = 12288;   // 48 KB of staged tokens
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -41,7 +39,9 @@ __device__ __forceinline__ void store_out(void* out, int dtype, size_t i, float 
   }
 }
 
-template <bool kWindow>
+// kQV, kAV: per-lane query and accumulator registers (32 kQV >= r + d_r, 32 kAV >= r). Four tokens'
+// dot products and their shuffles are under way together; the softmax then takes them one by one.
+template <bool kWindow, int kQV, int kAV>
 __global__ void __launch_bounds__(kThreads) simt_decode_kernel(const DecodeArgs a, int chunk) {
   extern __shared__ float tok[];   // [chunk][D]
   __shared__ WorkerPlan s_plan;
@@ -105,48 +105,60 @@ __global__ void __launch_bounds__(kThreads) simt_decode_kernel(const DecodeArgs 
       for (int c0 = t_begin; c0 < t_end; c0 += chunk) {
         const int cn = min(chunk, t_end - c0);
         __syncthreads();
-        for (int j = 0; j < cn; ++j) {
-          const int t = c0 + j;
+        // the chunk's values as one flat list over the block: the loads do not wait for one another
+#pragma unroll 4
+        for (int i = threadIdx.x; i < cn * D; i += kThreads) {
+          const int j = i / D, k = i - j * D, t = c0 + j;
           const int blk = checked_block(a.block_table, a.max_blocks, b, t / a.bs, a.num_blocks, a.status);
           const size_t slot = (size_t)blk * a.bs + (t % a.bs);
-          for (int k = threadIdx.x; k < D; k += kThreads) {
-            float v;
-            if (a.cache_dtype == kE4M3) {
-              if (k < a.r)
-                v = e4m3_to_float(__ldg((const uint8_t*)a.cache + slot * a.r + k)) * __ldg(a.kv_scale + slot);
-              else
-                v = bf16_bits_to_float(__ldg(a.k_rope + slot * a.d_r + (k - a.r)));
-            } else if (a.cache_dtype == kBF16) {
-              v = bf16_bits_to_float(__ldg((const uint16_t*)a.cache + slot * D + k));
-            } else {
-              v = __ldg((const float*)a.cache + slot * D + k);
-            }
-            tok[j * D + k] = v;
+          float v;
+          if (a.cache_dtype == kE4M3) {
+            if (k < a.r)
+              v = e4m3_to_float(__ldg((const uint8_t*)a.cache + slot * a.r + k)) * __ldg(a.kv_scale + slot);
+            else
+              v = bf16_bits_to_float(__ldg(a.k_rope + slot * a.d_r + (k - a.r)));
+          } else if (a.cache_dtype == kBF16) {
+            v = bf16_bits_to_float(__ldg((const uint16_t*)a.cache + slot * D + k));
+          } else {
+            v = __ldg((const float*)a.cache + slot * D + k);
           }
+          tok[i] = v;
         }
         __syncthreads();
         if (!row_ok) continue;
         const int jn = min(cn, hi - c0);
-        for (int j = 0; j < jn; ++j) {
-          if (kWindow && c0 + j < lo && c0 + j >= sink) continue;
-          const float* c = tok + j * D;
-          float d = 0.f;
+        constexpr int kT = 4;
+        for (int j0 = 0; j0 < jn; j0 += kT) {
+          float x[kT];
 #pragma unroll
-          for (int i = 0; i < kQV; ++i) {
-            const int k = lane + 32 * i;
-            if (k < D) d = fmaf(q[i], c[k], d);
-          }
-          const float x = warp_sum(d) * a.scale_log2;
-          const float m_new = fmaxf(m, x);
-          const float corr = exp2f(m - m_new);
-          const float p = exp2f(x - m_new);
-          l = fmaf(l, corr, p);
+          for (int u = 0; u < kT; ++u) {
+            const float* c = tok + min(j0 + u, jn - 1) * D;
+            float d = 0.f;
 #pragma unroll
-          for (int i = 0; i < kAV; ++i) {
-            const int k = lane + 32 * i;
-            if (k < a.r) acc[i] = fmaf(acc[i], corr, p * c[k]);
+            for (int i = 0; i < kQV; ++i) {
+              const int k = lane + 32 * i;
+              if (k < D) d = fmaf(q[i], c[k], d);
+            }
+            x[u] = d;
           }
-          m = m_new;
+#pragma unroll
+          for (int u = 0; u < kT; ++u) x[u] = warp_sum(x[u]) * a.scale_log2;
+#pragma unroll
+          for (int u = 0; u < kT; ++u) {
+            const int j = j0 + u;
+            if (j >= jn || (kWindow && c0 + j < lo && c0 + j >= sink)) continue;   // not seen by this row
+            const float* c = tok + j * D;
+            const float m_new = fmaxf(m, x[u]);
+            const float corr = exp2f(m - m_new);
+            const float p = exp2f(x[u] - m_new);
+            l = fmaf(l, corr, p);
+#pragma unroll
+            for (int i = 0; i < kAV; ++i) {
+              const int k = lane + 32 * i;
+              if (k < a.r) acc[i] = fmaf(acc[i], corr, p * c[k]);
+            }
+            m = m_new;
+          }
         }
       }
     }
@@ -359,7 +371,11 @@ cudaError_t launch_simt_decode(const DecodeArgs& a, cudaStream_t s) {
   if (chunk > 32) chunk = 32;
   if (chunk < 1) chunk = 1;
   dim3 grid(a.W, (a.rows + kWarps - 1) / kWarps);
-  auto kernel = a.window > 0 ? simt_decode_kernel<true> : simt_decode_kernel<false>;
+  // the registers of the widest shapes, or of those up to 128 wide (a tiny window of 24-wide rows:
+  // 57 us with 40 + 32 registers and one token at a time, 8 us like this)
+  constexpr int kWQ = kSimtMaxD / 32, kWA = kSimtMaxR / 32;
+  auto kernel = D <= 128 ? (a.window > 0 ? simt_decode_kernel<true, 4, 4> : simt_decode_kernel<false, 4, 4>)
+                         : (a.window > 0 ? simt_decode_kernel<true, kWQ, kWA> : simt_decode_kernel<false, kWQ, kWA>);
   kernel<<<grid, kThreads, sizeof(float) * chunk * D, s>>>(a, chunk);
   return cudaGetLastError();
 }

@@ -18,12 +18,12 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kVfThreads = 512;
+constexpr int kVfThreads = 256;
 constexpr int kVfWarps = kVfThreads / 32;
 constexpr int kVfChunk = 512;          // values per chunk
 constexpr int kVfPer = kVfChunk / 32;  // per lane
 constexpr int kVfMaxCluster = 8;
-constexpr int kVfMaxChunks = 2048;     // per CTA: V <= 2048 * 512 * 8 = 8 Mi
+constexpr int kVfMaxChunks = 2048;     // per CTA; V <= 2048 * 512 * 8 = 8 Mi
 
 struct VerifyArgs {
   int B, K, V;
@@ -73,7 +73,7 @@ __device__ __forceinline__ double weight(float p, float q) {
 
 // kVec: rows are whole 16-byte pieces (V a multiple of the values per piece, 16-byte aligned bases)
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs a) {
   constexpr int kPiece = 16 / (int)sizeof(T);
   __shared__ double chunk_sum[kVfMaxChunks];
   __shared__ double part[2];      // this CTA's sum, one slot per pass
@@ -305,9 +305,14 @@ extern "C" mla_status_t mla_verify_drafts(const mla_verify_params_t* p, const vo
   const VerifyArgs a{p->batch, p->max_drafts, p->vocab, target, draft, draft_tokens, draft_lens, accept_u, sample_u,
                      seq_lens, tokens, accepted, new_seq_lens, status};
   const bool vec = (size_t)p->vocab * e % 16 == 0 && ((uintptr_t)target | (uintptr_t)draft) % 16 == 0;
-  // one CTA per 4096 values, up to 8
-  int C = 1;
-  while (C < kVfMaxCluster && (int64_t)C * 4096 < p->vocab) C *= 2;
+  // CTAs per sequence: one per 4096 values (the loads that 8 warps issue at once), up to 8, but no more
+  // than it takes to give every SM its four: a longer slice hides the chain of dependent loads before it
+  int dev = 0, sms = 0, C = 1;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  while (C < kVfMaxCluster && (int64_t)C * 4096 < p->vocab && (int64_t)p->batch * C < 4 * sms) C *= 2;
+  // (a slice's chunk sums have to fit)
+  while (C < kVfMaxCluster && (int64_t)C * kVfMaxChunks * kVfChunk < p->vocab) C *= 2;
   const cudaError_t err = e == 4 ? launch<float>(a, vec, C, (cudaStream_t)stream)
                                  : launch<uint16_t>(a, vec, C, (cudaStream_t)stream);
   return err == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
