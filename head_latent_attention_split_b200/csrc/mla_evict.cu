@@ -12,11 +12,11 @@
 // shared-memory atomics bound it.
 //
 // Compact: a copy, bound by memory: every kept row read and written once. A warp takes 8 entries of
-// one sequence: 8 lanes look their slots up, then all lanes move the 8 rows side by side in
-// 16-byte pieces, so that a lane has 8 loads in flight and the warps of an SM do not wait for one
-// another.
+// one sequence; 8 lanes look their slots up and each moves its row by bulk copies through shared
+// memory, so the bytes in flight cost no registers (six CTAs of 37 KB per SM for a bf16 row of
+// 1152 bytes).
 #include <algorithm>
-#include <type_traits>
+#include <mutex>
 
 #include "mla_device.cuh"
 #include "ptx_sm100.cuh"
@@ -261,9 +261,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
 }
 
 // ------------------------------------------------------------------------------ compact
-constexpr int kCpThreads = 256;
+constexpr int kCpThreads = 128;
 constexpr int kCpRows = 8;                               // list entries per warp
 constexpr int kCpSpan = kCpRows * (kCpThreads / 32);     // ... and per CTA
+constexpr int kCpMaxSmem = 229376;
 
 struct CompactArgs {
   int bs, num_blocks, max_blocks, dst_blocks, list_stride, mass_stride, mass_out_stride, B;
@@ -280,11 +281,95 @@ struct CompactArgs {
   int* status;
 };
 
-// One warp copies rows src[i] -> dst[i] of one plane, V-sized pieces, eight loads in flight per
-// lane; dst < 0: skipped.
+// Lane i < 8 looks list entry j0 + i of sequence b up: its cache rows (dst < 0: none, or not to be
+// copied). The entry's scale and mass move at once.
+__device__ __forceinline__ void lookup(const CompactArgs& a, int b, int j0, int count, int& src, int& dst) {
+  const int lane = threadIdx.x & 31, j = j0 + lane;
+  src = 0;
+  dst = -1;
+  if (lane >= kCpRows) return;
+  float m = 0.f;
+  if (j < count) {
+    const int t = __ldg(a.indices + (size_t)b * a.list_stride + j);
+    const int db = __ldg(a.dst_table + (size_t)b * a.dst_blocks + j / a.bs);
+    const bool ok_t = t >= 0 && t < a.max_blocks * a.bs;
+    const int sb = ok_t ? __ldg(a.block_table + (size_t)b * a.max_blocks + t / a.bs) : -1;
+    const bool ok = sb >= 0 && sb < a.num_blocks && db >= 0 && db < a.num_blocks;
+    if (ok) {
+      src = sb * a.bs + t % a.bs;
+      dst = db * a.bs + j % a.bs;
+      if (a.kv_scale) a.kv_scale[dst] = a.kv_scale[src];
+    } else {
+      set_status(a.status, MLA_ERR_BAD_BLOCK_ID);
+    }
+    m = ok && a.mass && t < a.mass_stride ? __ldg(a.mass + (size_t)b * a.mass_stride + t) : __uint_as_float(0x7FC00000u);
+  }
+  if (a.mass && j < a.mass_out_stride) a.mass_out[(size_t)b * a.mass_out_stride + j] = m;
+}
+
+__device__ __forceinline__ int list_count(const CompactArgs& a, int b) {
+  int count = __ldg(a.counts + b);
+  if (count < 0 || count > a.list_stride) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, MLA_ERR_BAD_SEQ_LEN);
+    count = min(max(count, 0), a.list_stride);
+  }
+  return count;
+}
+
+// Rows of whole 16-byte pieces, up to 7 KB: each of the warp's 8 lanes sends its row through shared
+// memory with one bulk copy in and one out.
+__global__ void __launch_bounds__(kCpThreads) cache_compact_bulk_kernel(const CompactArgs a, const uint64_t timeout_ns) {
+  extern __shared__ __align__(128) uint8_t rows[];   // [kCpSpan][row_bytes + kr_bytes]
+  __shared__ uint64_t bar[kCpThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t mine = smem_u32(&bar[warp]);
+  if (lane == 0) {
+    mbar_init(mine, 1);
+    fence_mbarrier_init_cluster();
+    fence_proxy_async_smem();
+  }
+  __syncwarp();
+  const uint32_t kr = a.k_rope ? (uint32_t)a.kr_bytes : 0u, bytes = (uint32_t)a.row_bytes + kr;
+  const uint32_t buf = smem_u32(rows) + (uint32_t)(warp * kCpRows + min(lane, kCpRows - 1)) * bytes;
+  const int j0 = blockIdx.x * kCpSpan + warp * kCpRows;
+  uint32_t phase = 0;
+  int abort = 0;
+  for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
+    const int count = list_count(a, b);
+    int src, dst;
+    lookup(a, b, j0, count, src, dst);
+    const unsigned go = __ballot_sync(0xffffffffu, dst >= 0);
+    if (!go) continue;
+    if (lane == 0) mbar_arrive_expect_tx(mine, (uint32_t)__popc(go) * bytes);
+    __syncwarp();
+    if (dst >= 0) {
+      bulk_load(buf, a.cache + (size_t)src * a.row_bytes, a.row_bytes, mine);
+      if (kr) bulk_load(buf + a.row_bytes, a.k_rope + (size_t)src * kr, kr, mine);
+    }
+    const bool ok = __all_sync(0xffffffffu, mbar_wait<false>(mine, phase, &abort, timeout_ns));
+    if (!ok) {   // (copies in flight still write this buffer: wait for them without the short limit)
+      if (lane == 0) set_status(a.status, MLA_ERR_TIMEOUT);
+      int dummy = 0;
+      mbar_wait<false>(mine, phase, &dummy, kDrainTimeoutNs);
+      return;
+    }
+    phase ^= 1;
+    if (dst >= 0) {
+      bulk_store(a.cache + (size_t)dst * a.row_bytes, buf, a.row_bytes);
+      if (kr) bulk_store(a.k_rope + (size_t)dst * kr, buf + a.row_bytes, kr);
+      bulk_commit_group();
+      bulk_wait_group_read<0>();   // the buffer is read before it is filled again, or the CTA leaves
+    }
+    __syncwarp();
+  }
+}
+
+// Any rows: V-sized pieces (V divides both planes' rows and their bases' alignment) through registers,
+// eight loads in flight per lane.
 template <typename V>
 __device__ __forceinline__ void copy_rows(uint8_t* base, int row_bytes, const int* src, const int* dst) {
   const int per = row_bytes / (int)sizeof(V), lane = threadIdx.x & 31;
+#pragma unroll 1
   for (int i = lane; i < per; i += 32) {
     V v[kCpRows];
 #pragma unroll
@@ -296,40 +381,13 @@ __device__ __forceinline__ void copy_rows(uint8_t* base, int row_bytes, const in
   }
 }
 
-// kUnit: bytes per piece, dividing both planes' rows and their bases' alignment
-template <int kUnit>
+template <typename V>
 __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(const CompactArgs a) {
-  typedef typename std::conditional<kUnit == 16, uint4, typename std::conditional<kUnit == 4, uint32_t, uint8_t>::type>::type V;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int j0 = blockIdx.x * kCpSpan + warp * kCpRows;
+  const int j0 = blockIdx.x * kCpSpan + (threadIdx.x >> 5) * kCpRows;
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
-    int count = __ldg(a.counts + b);
-    if (count < 0 || count > a.list_stride) {
-      if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, MLA_ERR_BAD_SEQ_LEN);
-      count = min(max(count, 0), a.list_stride);
-    }
-    // lane i < 8 looks entry j0 + i up; its mass moves at once
-    const int j = j0 + lane;
-    int my_src = 0, my_dst = -1;
-    if (lane < kCpRows) {
-      float m = 0.f;
-      if (j < count) {
-        const int t = __ldg(a.indices + (size_t)b * a.list_stride + j);
-        const int db = __ldg(a.dst_table + (size_t)b * a.dst_blocks + j / a.bs);
-        const bool ok_t = t >= 0 && t < a.max_blocks * a.bs;
-        const int sb = ok_t ? __ldg(a.block_table + (size_t)b * a.max_blocks + t / a.bs) : -1;
-        const bool ok = sb >= 0 && sb < a.num_blocks && db >= 0 && db < a.num_blocks;
-        if (ok) {
-          my_src = sb * a.bs + t % a.bs;
-          my_dst = db * a.bs + j % a.bs;
-          if (a.kv_scale) a.kv_scale[my_dst] = a.kv_scale[my_src];
-        } else {
-          set_status(a.status, MLA_ERR_BAD_BLOCK_ID);
-        }
-        m = ok && a.mass && t < a.mass_stride ? __ldg(a.mass + (size_t)b * a.mass_stride + t) : __uint_as_float(0x7FC00000u);
-      }
-      if (a.mass && j < a.mass_out_stride) a.mass_out[(size_t)b * a.mass_out_stride + j] = m;
-    }
+    const int count = list_count(a, b);
+    int my_src, my_dst;
+    lookup(a, b, j0, count, my_src, my_dst);
     if (j0 >= count) continue;
     int src[kCpRows], dst[kCpRows];
 #pragma unroll
@@ -433,12 +491,24 @@ mla_status_t mla_cache_compact(const mla_compact_params_t* p, void* kv_cache, vo
   const int span = mass ? p->mass_out_stride : p->list_stride;
   const dim3 grid((unsigned)((span + kCpSpan - 1) / kCpSpan), (unsigned)std::min(p->batch, 65535));
   cudaStream_t s = (cudaStream_t)stream;
-  if (fits(16))
-    cache_compact_kernel<16><<<grid, kCpThreads, 0, s>>>(a);
-  else if (fits(4))
-    cache_compact_kernel<4><<<grid, kCpThreads, 0, s>>>(a);
-  else
-    cache_compact_kernel<1><<<grid, kCpThreads, 0, s>>>(a);
+  const int row_smem = kCpSpan * (a.row_bytes + (a.k_rope ? a.kr_bytes : 0));
+  if (fits(16) && row_smem <= kCpMaxSmem) {
+    static std::once_flag once[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    cudaError_t err = cudaSuccess;
+    std::call_once(once[dev & 63], [&] {
+      err = cudaFuncSetAttribute(cache_compact_bulk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCpMaxSmem);
+    });
+    if (err != cudaSuccess) return MLA_ERR_CUDA;
+    cache_compact_bulk_kernel<<<grid, kCpThreads, row_smem, s>>>(a, wait_timeout_ns());
+  } else if (fits(16)) {
+    cache_compact_kernel<uint4><<<grid, kCpThreads, 0, s>>>(a);
+  } else if (fits(4)) {
+    cache_compact_kernel<uint32_t><<<grid, kCpThreads, 0, s>>>(a);
+  } else {
+    cache_compact_kernel<uint8_t><<<grid, kCpThreads, 0, s>>>(a);
+  }
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

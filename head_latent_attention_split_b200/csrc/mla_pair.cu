@@ -183,6 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int* abort = &ctl.abort;
   typedef SegmentIterT<typename TilesOf<kWindow>::type> SegIter;
   const auto tiles = TilesOf<kWindow>::make(a);
+  if constexpr (kWindow) launch_dependents();   // the combine
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlotsS; ++i) {
@@ -398,6 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     while (it.next(sg)) {
       const int n = sg.tile_end - sg.tile_begin;
       float m_run = -INFINITY, l_run = 0.f, l_tot = 0.f;   // l_run: this half's columns
+      bool poisoned = false;
       if (ok) {
         // this segment's absorbed query into TMEM, one row per thread pair: half 0 loads the
         // latent channels [0, 256), half 1 the channels [256, 512) and the RoPE channels
@@ -438,6 +440,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_before();
           warp_arrive(smem_u32(&ctl.q_full));
         }
+        // (here, while the first pair is scored: its loads would hold the next segment up)
+        poisoned = segment_poisoned(a, tiles, sg.b, sg.tile_begin, sg.tile_end);
         int n_row = valid_row ? (a.causal ? sg.Lc - a.Sq + 1 + s_idx : sg.Lc) : 0;
         if (n_row < 0) n_row = 0;
         for (int li = 0; ok && li < n; li += 2, ++u) {
@@ -555,7 +559,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++seg;
       }
       // log-sum-exp of the rows of this segment (the output CTA writes the values)
-      const bool poisoned = segment_poisoned(a, tiles, sg.b, sg.tile_begin, sg.tile_end);
       if (valid_row && half == 0) {
         float lse_v = l_tot > 0.f ? (m_run + log2f(l_tot)) * 0.69314718055994531f : -INFINITY;
         if (!ok || poisoned) lse_v = __uint_as_float(0x7FC00000u);
@@ -729,6 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     while (it.next(sg)) {
       const int n = sg.tile_end - sg.tile_begin;
       float inv_l = 0.f;
+      const bool poisoned = segment_poisoned(a, tiles, sg.b, sg.tile_begin, sg.tile_end);   // before the first message
       if (ok) {
         const int last_tile = tiles.count(sg.Lc) - 1;
         const int tail = sg.Lc % kBS;
@@ -811,7 +815,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (ok) ok = wait_warp(smem_u32(&ctl.pv_done[(t - 1) % kRxBufs]), ((t - 1) / kRxBufs) & 1);
       }
       // epilogue: O / l -> out (single split) or the normalised partial (several splits)
-      const bool poisoned = segment_poisoned(a, tiles, sg.b, sg.tile_begin, sg.tile_end);
       const bool nan_rows = !ok || poisoned;
       const bool direct = sg.splits == 1;
       const size_t qrow = (size_t)sg.b * a.rows + grow;

@@ -10,6 +10,7 @@
 #include <cmath>
 
 #include "mla_device.cuh"
+#include "ptx_sm100.cuh"
 
 namespace mla {
 namespace {
@@ -53,6 +54,7 @@ __global__ void __launch_bounds__(kThreads) simt_decode_kernel(const DecodeArgs 
   const int s = row_ok ? row / a.H : 0;
   const int cap = a.len_cap;
   const auto tiles = TilesOf<kWindow>::make(a);   // windowed: only the blocks that some row sees
+  if constexpr (kWindow) ptx::launch_dependents();   // the combine
 
   if (warp == 0) {
     WorkerPlan p = warp_plan(a.seq_lens, a.B, tiles, cap, a.W, w, a.status);
@@ -191,6 +193,10 @@ __global__ void __launch_bounds__(kThreads) simt_decode_kernel(const DecodeArgs 
 // workspace is trusted for indexing). Rows of a sequence with a seq_len out of range, and rows
 // whose partials carry a NaN log-sum-exp (a decode wait timed out, or a bad block id), are
 // written as NaN.
+// A chain of latencies bounds it (a few MB of partials, in L2): lengths, log-sum-exps, partials. So the
+// window decode launches it as a dependent of the decode kernel, with the lengths read and the
+// split found while that kernel still runs, and the partials of the first splits are requested before
+// their weights are known.
 template <bool kWindow>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
   __shared__ long long s_sum[kWarps][2];
@@ -223,30 +229,42 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
     total += s_sum[i][1];
   }
   const int row = blockIdx.y * kWarps + warp;
-  if (row >= a.rows) return;
   const size_t orow = (size_t)b * a.rows + row;
   const int raw = __ldg(a.seq_lens + b);
   const float qnan = __uint_as_float(0x7FC00000u);
-  if (raw < 0 || raw > cap) {
-    for (int k = lane; k < a.r; k += 32) store_out(a.out, a.out_dtype, orow * a.r + k, qnan);
-    if (lane == 0) a.lse[orow] = qnan;
+  const long long n = raw < 0 || raw > cap ? 0 : tiles.count(raw);
+  int first = 0, splits = 0;
+  if (n > 0) {
+    const int Wa = (total < a.W) ? (int)total : a.W;
+    first = worker_of_tile(before, total, Wa);
+    splits = worker_of_tile(before + n - 1, total, Wa) - first + 1;
+  }
+  if constexpr (kWindow) ptx::wait_for_grid_before();   // every thread, so that this grid ends after the decode's
+  if (row >= a.rows || splits == 1) return;             // (one split: the decode wrote the row directly)
+  if (splits == 0) {
+    const bool bad = raw < 0 || raw > cap;
+    for (int k = lane; k < a.r; k += 32) store_out(a.out, a.out_dtype, orow * a.r + k, bad ? qnan : 0.f);
+    if (lane == 0) a.lse[orow] = bad ? qnan : -INFINITY;
     return;
   }
-  const long long n = tiles.count(raw);
-  if (n == 0) {
-    for (int k = lane; k < a.r; k += 32) store_out(a.out, a.out_dtype, orow * a.r + k, 0.f);
-    if (lane == 0) a.lse[orow] = -INFINITY;
-    return;
-  }
-  const int Wa = (total < a.W) ? (int)total : a.W;
-  const int first = worker_of_tile(before, total, Wa);
-  const int splits = worker_of_tile(before + n - 1, total, Wa) - first + 1;
-  if (splits <= 1) return;   // the decode wrote this row directly
   const size_t slot0 = (size_t)first + b;
-  float M = -INFINITY;
+  const bool vec = a.r % 4 == 0;
+  // the first two splits' pieces of the first 512 channels (see below), requested at once
+  float4 early[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = 4 * lane + 128 * u;
+      early[i][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (vec && k < a.r) early[i][u] = *reinterpret_cast<const float4*>(a.o_part + ((slot0 + i) * a.rows + row) * a.r + k);
+    }
+  }
+  float M = -INFINITY, mine = -INFINITY;   // mine: the log-sum-exp of split `lane`
   bool has_nan = false;
   for (int i = lane; i < splits; i += 32) {
     const float v = a.lse_part[(slot0 + i) * a.rows + row];
+    if (i == lane) mine = v;
     has_nan |= v != v;
     M = fmaxf(M, v);
   }
@@ -263,14 +281,14 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
     return;
   }
   float Z = 0.f;
-  for (int i = lane; i < splits; i += 32) Z += expf(a.lse_part[(slot0 + i) * a.rows + row] - M);
+  for (int i = lane; i < splits; i += 32) Z += expf((i == lane ? mine : a.lse_part[(slot0 + i) * a.rows + row]) - M);
   Z = warp_sum(Z);
   const float lse_v = M + logf(Z);
-  if (a.r % 4 == 0) {
+  if (vec) {
     // 512 channels per pass, 16 per lane as four float4 pieces; each split's pieces are
     // independent loads, so a split costs one memory latency, not one per piece. The split
     // weights come from lane i (splits <= 32) by shuffle; the output goes out 4 channels per store.
-    const float wl = lane < splits ? expf(a.lse_part[(slot0 + lane) * a.rows + row] - lse_v) : 0.f;
+    const float wl = lane < splits ? expf(mine - lse_v) : 0.f;
     // 4 output channels per store when the output allows it (the SIMT path takes 4-byte
     // aligned outputs)
     const bool vec_out = ((uintptr_t)a.out % (a.out_dtype == kF32 ? 16u : 8u)) == 0;
@@ -278,23 +296,37 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
       float4 o[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](float wgt, const float4* v) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          o[u].x = fmaf(wgt, v[u].x, o[u].x);
+          o[u].y = fmaf(wgt, v[u].y, o[u].y);
+          o[u].z = fmaf(wgt, v[u].z, o[u].z);
+          o[u].w = fmaf(wgt, v[u].w, o[u].w);
+        }
+      };
+      int i0 = 0;
+      if (k0 == 0) {   // (splits >= 2)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float wgt = __shfl_sync(0xffffffffu, wl, i);
+          if (wgt != 0.f) add(wgt, early[i]);
+        }
+        i0 = 2;
+      }
 #pragma unroll 2
-      for (int i = 0; i < splits; ++i) {
+      for (int i = i0; i < splits; ++i) {
         const size_t prow = (slot0 + i) * a.rows + row;
         const float wgt = i < 32 ? __shfl_sync(0xffffffffu, wl, i) : expf(a.lse_part[prow] - lse_v);
         if (wgt == 0.f) continue;
         const float* src = a.o_part + prow * a.r;
+        float4 v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int k = k0 + 4 * lane + 128 * u;
-          if (k < a.r) {
-            const float4 v = *reinterpret_cast<const float4*>(src + k);
-            o[u].x = fmaf(wgt, v.x, o[u].x);
-            o[u].y = fmaf(wgt, v.y, o[u].y);
-            o[u].z = fmaf(wgt, v.z, o[u].z);
-            o[u].w = fmaf(wgt, v.w, o[u].w);
-          }
+          v[u] = k < a.r ? *reinterpret_cast<const float4*>(src + k) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        add(wgt, v);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -382,8 +414,20 @@ cudaError_t launch_simt_decode(const DecodeArgs& a, cudaStream_t s) {
 
 cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t s) {
   dim3 grid(a.B, (a.rows + kWarps - 1) / kWarps);
-  auto kernel = a.window > 0 ? combine_kernel<true> : combine_kernel<false>;
-  kernel<<<grid, kThreads, 0, s>>>(a);
+  if (a.window > 0) {
+    // a dependent of the decode kernel before it: its blocks may start while that kernel's last CTAs run
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, combine_kernel<true>, a);
+  }
+  combine_kernel<false><<<grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

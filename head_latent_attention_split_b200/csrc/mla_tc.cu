@@ -214,6 +214,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
   volatile int* abort = &ctl.abort;
   typedef SegmentIterT<typename TilesOf<kWindow>::type> SegIter;
   const auto tiles = TilesOf<kWindow>::make(a);   // windowed: only the blocks that some row sees
+  if constexpr (kWindow) launch_dependents();      // the combine
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -643,6 +644,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
         tc_fence_before();
         mbar_arrive(smem_u32(&ctl.q_full));
       }
+      // (here, while the first tile is scored: its loads would hold the epilogue up)
+      const bool poisoned = segment_poisoned(a, tiles, sg.b, sg.tile_begin, sg.tile_end);
       const int n = sg.tile_end - sg.tile_begin;
       const int last_tile = tiles.count(sg.Lc) - 1;
       float m_run = -INFINITY, l_run = 0.f;   // own rows: running maximum (log2 units), this thread's sum
@@ -919,7 +922,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
         __syncwarp();
         if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.lrx_full[seg & 1]), kLrxBytes);   // segment seg + 2
       }
-      const bool poisoned = segment_poisoned(a, tiles, sg.b, sg.tile_begin, sg.tile_end);
       const float inv = poisoned ? __uint_as_float(0x7FC00000u) : l_tot > 0.f ? 1.f / l_tot : 0.f;
       const size_t qrow = (size_t)sg.b * a.rows + grow;
       const bool direct = sg.splits == 1;

@@ -3,13 +3,15 @@
 // CDF, and the sequence's new length.
 //
 // Only one row of each distribution is read, the one behind the last accepted draft, so a sequence
-// costs 2 V values. A cluster of C CTAs shares it. The row is cut into chunks of 512
-// values; a warp sums a chunk (16 weights per lane, all loads issued together) and the chunk
-// sums stay in shared memory. One exchange of the CTAs' sums gives the total, the draw's target
+// costs 2 V values. A cluster of C CTAs shares it. The row is cut into chunks of 1024
+// values; a warp sums a chunk (32 weights per lane, the next 8 pairs on their way while 8 are added)
+// and the chunk sums stay in shared memory. One exchange of the CTAs' sums gives the total, the draw's target
 // and the CTA that holds it, which finds the chunk among its sums and reads that chunk again.
 // All sums are fp64: the weights are fp32 or bf16 and the draw has to fall on the same token
 // whatever the order of the sum, so its rounding must be far below a weight. Every CTA adds in the
 // same order (chunk, prefix of chunks, prefix of CTAs): the result does not vary between runs.
+#include <type_traits>
+
 #include "mla_device.cuh"
 #include "ptx_sm100.cuh"
 
@@ -20,10 +22,12 @@ using namespace ptx;
 
 constexpr int kVfThreads = 256;
 constexpr int kVfWarps = kVfThreads / 32;
-constexpr int kVfChunk = 512;          // values per chunk
-constexpr int kVfPer = kVfChunk / 32;  // per lane
+constexpr int kVfChunk = 1024;         // values per chunk
+constexpr int kVfPer = kVfChunk / kVfThreads;   // per thread when a chunk is searched
+constexpr int kNone = 0x7fffffff;
+constexpr double kMaxDouble = 1.7976931348623157e308;
 constexpr int kVfMaxCluster = 8;
-constexpr int kVfMaxChunks = 2048;     // per CTA; V <= 2048 * 512 * 8 = 8 Mi
+constexpr int kVfMaxChunks = 1024;     // per CTA; V <= 1024 * 1024 * 8 = 8 Mi
 
 struct VerifyArgs {
   int B, K, V;
@@ -71,13 +75,63 @@ __device__ __forceinline__ double weight(float p, float q) {
   return w > 0.0 ? w : 0.0;
 }
 
-// kVec: rows are whole 16-byte pieces (V a multiple of the values per piece, 16-byte aligned bases)
+// One lane's part of kCount = 32 x kPer consecutive values of a row pair: loaded, then added.
+// kVec: rows are whole 16-byte pieces (V a multiple of the values per piece, 16-byte aligned bases).
+template <typename T, bool kVec>
+struct Unit {
+  static constexpr int kPiece = kVec ? 16 / (int)sizeof(T) : 1, kLoads = kVec ? 2 : 8;
+  static constexpr int kCount = 32 * kPiece * kLoads;
+  typedef typename std::conditional<kVec, uint4, T>::type Word;
+  Word p[kLoads], q[kLoads];
+
+  __device__ __forceinline__ void load(const T* pr, const T* qr, int base, int V) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) {
+      const int i = base + (32 * l + lane) * kPiece;
+      p[l] = q[l] = Word();
+      if (i < V) {
+        p[l] = __ldg(reinterpret_cast<const Word*>(pr + i));
+        if (qr) q[l] = __ldg(reinterpret_cast<const Word*>(qr + i));
+      }
+    }
+  }
+  static __device__ __forceinline__ float value(const Word& w, int e) {
+    if constexpr (kVec) {
+      const uint32_t x = (e * (int)sizeof(T)) / 4 == 0 ? w.x : (e * (int)sizeof(T)) / 4 == 1 ? w.y
+                         : (e * (int)sizeof(T)) / 4 == 2 ? w.z : w.w;
+      return __uint_as_float(sizeof(T) == 4 ? x : e & 1 ? x & 0xFFFF0000u : x << 16);
+    } else if constexpr (sizeof(T) == 4) {
+      return w;
+    } else {
+      return bf16_bits_to_float(w);
+    }
+  }
+  // Two running sums, for the length of the chain of additions. kCareful: as weight() says, and
+  // without the token `hole`; otherwise max(p, q) - q, the same number for finite p and q (and
+  // NaN or an infinity in the sum where they are not).
+  template <bool kCareful>
+  __device__ __forceinline__ void add(double& s0, double& s1, int base, int hole) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) {
+      const int i = base + (32 * l + lane) * kPiece;
+#pragma unroll
+      for (int e = 0; e < kPiece; ++e) {
+        const float x = value(p[l], e), y = value(q[l], e);
+        const double w = kCareful ? (i + e == hole ? 0.0 : weight(x, y)) : (double)fmaxf(x, y) - (double)y;
+        if ((l * kPiece + e) & 1) s1 += w; else s0 += w;
+      }
+    }
+  }
+};
+
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs a) {
-  constexpr int kPiece = 16 / (int)sizeof(T);
   __shared__ double chunk_sum[kVfMaxChunks];
-  __shared__ double part[2];      // this CTA's sum, one slot per pass
-  __shared__ int s_n, s_tok;
+  __shared__ double part[3];      // this CTA's sum, one slot per pass
+  __shared__ double warp_sum[kVfWarps];
+  __shared__ int s_n, s_tok, s_at, s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t C, rank = cluster_ctarank();
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
@@ -117,13 +171,14 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs 
     if (lane == 0) {
       s_n = n;
       s_tok = tok;
+      s_at = kNone;
+      s_last = -1;
     }
   }
   __syncthreads();
   int n = s_n;
   const int tok = s_tok;   // the refused draft (draft null: its weight is 0)
   bool bad = bad_len || n < 0;
-  int got = -1;
 
   if (!bad) {   // the same branch in every CTA of the cluster
     const T* p = target + (size_t)n * V;
@@ -134,57 +189,38 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs 
     float u = __ldg(a.sample_u + b);
     u = u >= 1.f ? 0x1.fffffep-1f : u >= 0.f ? u : 0.f;
     double before = 0.0, total = 0.0;
-    bool residual = refused;
+    bool residual = refused, careful = false;
+    int pass = 0;
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-      // pass 1 only when the residual is 0 everywhere: the target's own row
+    for (;; ++pass) {
+      // One pass, as a rule. Again with care when the sum is not finite; again over the target's own row
+      // when the residual is 0 everywhere: three at most.
       const T* qq = residual ? q : nullptr;
       const int hole = residual && !draft ? tok : -1;
-      for (int c = c0 + warp; c < c1; c += kVfWarps) {
-        const int base = c * kVfChunk;
-        double s = 0.0;
-        if constexpr (kVec) {
-          constexpr int kLoads = kVfPer / kPiece;
-          uint4 pv[kLoads], qv[kLoads];
+      // this warp's chunks as one stream of units, the next one loading while one is added
+      typedef Unit<T, kVec> U;
+      constexpr int kUnits = kVfChunk / U::kCount;
+      const int mine_chunks = c0 + warp < c1 ? (c1 - c0 - warp + kVfWarps - 1) / kVfWarps : 0;
+      auto unit_base = [&](int i) { return (c0 + warp + (i / kUnits) * kVfWarps) * kVfChunk + (i % kUnits) * U::kCount; };
+      U buf[2];
+      double sa = 0.0, sb = 0.0;
+      if (mine_chunks > 0) buf[0].load(p, qq, unit_base(0), V);
+#pragma unroll 1
+      for (int i = 0; i < mine_chunks * kUnits; i += 2) {   // kUnits is even
 #pragma unroll
-          for (int l = 0; l < kLoads; ++l) {
-            const int i = base + (32 * l + lane) * kPiece;
-            pv[l] = qv[l] = make_uint4(0u, 0u, 0u, 0u);
-            if (i < V) {
-              pv[l] = __ldg(reinterpret_cast<const uint4*>(p + i));
-              if (qq) qv[l] = __ldg(reinterpret_cast<const uint4*>(qq + i));
-            }
-          }
-#pragma unroll
-          for (int l = 0; l < kLoads; ++l) {
-            const int i = base + (32 * l + lane) * kPiece;
-            const uint32_t pw[4] = {pv[l].x, pv[l].y, pv[l].z, pv[l].w}, qw[4] = {qv[l].x, qv[l].y, qv[l].z, qv[l].w};
-#pragma unroll
-            for (int e = 0; e < kPiece; ++e) {
-              float x, y;
-              if constexpr (sizeof(T) == 4) {
-                x = __uint_as_float(pw[e]);
-                y = __uint_as_float(qw[e]);
-              } else {
-                x = __uint_as_float(e & 1 ? pw[e >> 1] & 0xFFFF0000u : pw[e >> 1] << 16);
-                y = __uint_as_float(e & 1 ? qw[e >> 1] & 0xFFFF0000u : qw[e >> 1] << 16);
-              }
-              s += i + e == hole ? 0.0 : weight(x, y);
-            }
-          }
-        } else {
-          float x[kVfPer], y[kVfPer];
-#pragma unroll
-          for (int e = 0; e < kVfPer; ++e) {
-            const int i = base + 32 * e + lane;
-            x[e] = i < V ? prob(p, i) : 0.f;
-            y[e] = i < V && qq ? prob(qq, i) : 0.f;
-          }
-#pragma unroll
-          for (int e = 0; e < kVfPer; ++e) s += base + 32 * e + lane == hole ? 0.0 : weight(x[e], y[e]);
+        for (int h = 0; h < 2; ++h) {
+          if (i + h + 1 < mine_chunks * kUnits) buf[h ^ 1].load(p, qq, unit_base(i + h + 1), V);
+          const int ub = unit_base(i + h);
+          if (careful || (hole >= ub && hole < ub + U::kCount))
+            buf[h].template add<true>(sa, sb, ub, hole);
+          else
+            buf[h].template add<false>(sa, sb, ub, hole);
         }
-        s = warp_sum64(s);
-        if (lane == 0) chunk_sum[c - c0] = s;
+        if ((i + 2) % kUnits == 0) {
+          const double s = warp_sum64(sa + sb);
+          if (lane == 0) chunk_sum[warp + (i / kUnits) * kVfWarps] = s;
+          sa = sb = 0.0;
+        }
       }
       __syncthreads();
       if (warp == 0) {
@@ -205,21 +241,26 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs 
         if (r == rank) before = total;
         total += v;
       }
-      if (total > 0.0 || !residual) break;
-      residual = false;
+      if (!careful && !(total <= kMaxDouble)) {
+        careful = true;
+      } else if (total > 0.0 || !residual) {
+        break;
+      } else {
+        residual = false;
+      }
     }
-    bad = !(total > 0.0 && total <= 1.7976931348623157e308);
+    bad = !(total > 0.0 && total <= kMaxDouble);
     const double goal = (double)u * total;
     // the CTA whose range [before, before + own sum) holds the goal; the same additions in every CTA
-    const bool mine = !bad && before <= goal && goal < before + part[residual || !refused ? 0 : 1];
-    if (mine && warp == 0) {
+    const bool mine = !bad && before <= goal && goal < before + part[pass];
+    if (mine) {   // the whole block: one chunk, four consecutive values per thread
       int lo = 0, hi = c1 - c0 - 1;   // first chunk whose prefix exceeds the goal
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (before + chunk_sum[mid] > goal) hi = mid; else lo = mid + 1;
       }
-      double run = before + (lo > 0 ? chunk_sum[lo - 1] : 0.0);
-      const int base = (c0 + lo) * kVfChunk + lane * kVfPer;   // 16 consecutive values per lane
+      const double run = before + (lo > 0 ? chunk_sum[lo - 1] : 0.0);
+      const int base = (c0 + lo) * kVfChunk + tid * kVfPer;
       const T* qq = residual ? q : nullptr;
       const int hole = residual && !draft ? tok : -1;
       double w[kVfPer], s = 0.0;
@@ -229,22 +270,30 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs 
         w[e] = i < V && i != hole ? weight(prob(p, i), qq ? prob(qq, i) : 0.f) : 0.0;
         s += w[e];
       }
-      const double upto = run + warp_scan64(s);
-      run = upto - s;
-      int at = -1, last = -1;   // first value past the goal; last one with a weight
+      const double incl = warp_scan64(s);
+      if (lane == 31) warp_sum[warp] = incl;
+      __syncthreads();
+      double upto = run;
+      for (int i = 0; i < warp; ++i) upto += warp_sum[i];
+      upto += incl - s;
+      int at = kNone, last = -1;   // first value past the goal; last one with a weight
 #pragma unroll
       for (int e = 0; e < kVfPer; ++e) {
-        run += w[e];
+        upto += w[e];
         if (w[e] > 0.0) {
           last = base + e;
-          if (at < 0 && run > goal) at = base + e;
+          if (at == kNone && upto > goal) at = base + e;
         }
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, at >= 0), any = __ballot_sync(0xffffffffu, last >= 0);
+      at = __reduce_min_sync(0xffffffffu, at);
+      last = __reduce_max_sync(0xffffffffu, last);
+      if (lane == 0) {
+        atomicMin(&s_at, at);
+        atomicMax(&s_last, last);
+      }
+      __syncthreads();
       // (the sums inside the chunk round differently from its prefix: without a hit, its last weight)
-      got = hit ? __shfl_sync(0xffffffffu, at, __ffs(hit) - 1)
-                : __shfl_sync(0xffffffffu, last, any ? 31 - __clz(any) : 0);
-      if (lane == 0) a.out[(size_t)b * (K + 1) + n] = got;
+      if (tid == 0) a.out[(size_t)b * (K + 1) + n] = s_at != kNone ? s_at : s_last;
     }
   }
   if (rank == 0) {
@@ -305,12 +354,13 @@ extern "C" mla_status_t mla_verify_drafts(const mla_verify_params_t* p, const vo
   const VerifyArgs a{p->batch, p->max_drafts, p->vocab, target, draft, draft_tokens, draft_lens, accept_u, sample_u,
                      seq_lens, tokens, accepted, new_seq_lens, status};
   const bool vec = (size_t)p->vocab * e % 16 == 0 && ((uintptr_t)target | (uintptr_t)draft) % 16 == 0;
-  // CTAs per sequence: one per 4096 values (the loads that 8 warps issue at once), up to 8, but no more
-  // than it takes to give every SM its four: a longer slice hides the chain of dependent loads before it
+  // CTAs per sequence: one per 4096 values (what 8 warps load at once), up to 8, but no more than it
+  // takes to give every SM two: a longer slice hides the chain of dependent loads before it (128
+  // sequences of 128000 values: 40 us with 8, 35 us with 4, 41 us with 2)
   int dev = 0, sms = 0, C = 1;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return MLA_ERR_CUDA;
-  while (C < kVfMaxCluster && (int64_t)C * 4096 < p->vocab && (int64_t)p->batch * C < 4 * sms) C *= 2;
+  while (C < kVfMaxCluster && (int64_t)C * 4096 < p->vocab && (int64_t)p->batch * C < 2 * sms) C *= 2;
   // (a slice's chunk sums have to fit)
   while (C < kVfMaxCluster && (int64_t)C * kVfMaxChunks * kVfChunk < p->vocab) C *= 2;
   const cudaError_t err = e == 4 ? launch<float>(a, vec, C, (cudaStream_t)stream)
