@@ -401,40 +401,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float m_run = -INFINITY, l_run = 0.f, l_tot = 0.f;   // l_run: this half's columns
       bool poisoned = false;
       if (ok) {
-        // this segment's absorbed query into TMEM, one row per thread pair: half 0 loads the
-        // latent channels [0, 256), half 1 the channels [256, 512) and the RoPE channels
+        // this segment's absorbed query into TMEM: of every row, half 0 loads the latent channels
+        // [0, 256), half 1 the channels [256, 512) and the RoPE channels
         ok = wait_warp(smem_u32(&ctl.q_empty), (seg & 1) ^ 1);
         if (ok) {
-          const size_t qoff = (size_t)sg.b * a.rows + (valid_row ? grow : 0);
-          const uint4* ql = reinterpret_cast<const uint4*>((const uint16_t*)a.q_lat + qoff * kR) + 32 * half;
-          const uint4* qr = reinterpret_cast<const uint4*>((const uint16_t*)a.q_rope + qoff * kDR);
-          const int nq = half ? 40 : 32;   // 16-byte pieces of this thread's share (multiples of 8)
-#pragma unroll 1
-          for (int r0 = 0; r0 < nq; r0 += 16) {
-            uint4 qv[16];
+          // in blocks of 128 bytes per row: eight lanes read a row's block side by side (instruction i:
+          // row 8 (lane / 8) + i, piece lane % 8), then the pieces move to the row's own lane. Read one
+          // row per lane, this took 6-8 us of LSU requests instead of about 2.
+          const int row0 = rg * kRows + 32 * quarter + (lane & ~7);   // query row of this lane group's first row
+          const uint16_t* ql = (const uint16_t*)a.q_lat + ((size_t)sg.b * a.rows + row0) * kR + 256 * half + 8 * (lane & 7);
+          const uint16_t* qr = (const uint16_t*)a.q_rope + ((size_t)sg.b * a.rows + row0) * kDR + 8 * (lane & 7);
+          const int nb = half ? 5 : 4;   // half 1 loads the RoPE channels too
+          auto fetch = [&](int k, uint4 (&q)[8]) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int k = r0 + i;
-              qv[i] = (valid_row && k < nq) ? __ldg(k < 32 ? ql + k : qr + (k - 32)) : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 8; ++i)
+              q[i] = row0 + i < a.rows
+                         ? __ldg(reinterpret_cast<const uint4*>(k < 4 ? ql + (size_t)i * kR + 64 * k : qr + (size_t)i * kDR))
+                         : make_uint4(0u, 0u, 0u, 0u);
+          };
+          uint4 qv[2][8];
+          fetch(0, qv[0]);
+#pragma unroll
+          for (int k = 0; k < 5; ++k) {
+            if (k >= nb) break;
+            if (k + 1 < nb) fetch(k + 1, qv[(k + 1) & 1]);
+            uint4 (&q)[8] = qv[k & 1];
+            transpose_pieces<8>(q);
+            uint32_t w32[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              w32[4 * i] = q[i].x;
+              w32[4 * i + 1] = q[i].y;
+              w32[4 * i + 2] = q[i].z;
+              w32[4 * i + 3] = q[i].w;
             }
-#pragma unroll
-            for (int g = 0; g < 16; g += 8) {
-              const int k = r0 + g;   // first piece of this group of 8 (32 columns)
-              if (k < nq) {
-                uint32_t w32[32];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  w32[4 * i] = qv[g + i].x;
-                  w32[4 * i + 1] = qv[g + i].y;
-                  w32[4 * i + 2] = qv[g + i].z;
-                  w32[4 * i + 3] = qv[g + i].w;
-                }
-                // piece k holds query words 4 k .. 4 k + 3 of this half's latent block, or (k >= 32)
-                // the RoPE words 4 (k - 32) .. ; column = word index
-                const uint32_t col = k < 32 ? 128 * half + 4 * k : 256 + 4 * (k - 32);
-                tmem_st32(tmem + lane_off + kTmemQ + col, w32);
-              }
-            }
+            // column = word index of the absorbed query row
+            tmem_st32(tmem + lane_off + kTmemQ + (k < 4 ? 128 * half + 32 * k : 256), w32);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -817,31 +819,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // epilogue: O / l -> out (single split) or the normalised partial (several splits)
       const bool nan_rows = !ok || poisoned;
       const bool direct = sg.splits == 1;
-      const size_t qrow = (size_t)sg.b * a.rows + grow;
-      const size_t prow = (size_t)(w + sg.b) * a.rows + grow;
       if (ok) tc_fence_after();
-#pragma unroll 1
-      for (int cc = 0; cc < 8; ++cc) {
+      // Eight lanes write 128 bytes of a row side by side (transpose_pieces): the row of instruction i is
+      // the group's i-th. One row per lane took 11 us for 128 x 512 fp32 (LSU requests), this about 2.
+      const int row0 = rg * kRows + 32 * quarter + (lane & ~7);
+      const size_t qrow0 = (size_t)sg.b * a.rows + row0, prow0 = (size_t)(w + sg.b) * a.rows + row0;
+      const bool bf16_out = direct && a.out_dtype == kBF16;
+      auto load32 = [&](int cc, float* f) {
         uint32_t v[32];
         if (ok) {
           tmem_ld32(tmem + lane_off + col0 + 32 * cc, v);
           tmem_wait_ld();
         }
-        if (!valid_row) continue;
-        float f[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) f[i] = nan_rows ? __uint_as_float(0x7FC00000u) : __uint_as_float(v[i]) * inv_l;
-        const int ch = col0 + 32 * cc;
-        if (direct && a.out_dtype == kBF16) {
-          uint4* dst = reinterpret_cast<uint4*>((uint16_t*)a.out + qrow * kR + ch);
+      };
+      if (bf16_out) {
+#pragma unroll 1
+        for (int cc = 0; cc < 8; cc += 2) {
+          uint4 u[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]), pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
-                                pack_bf16x2(f[8 * i + 4], f[8 * i + 5]), pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
-        } else {
-          float4* dst = reinterpret_cast<float4*>(direct ? (float*)a.out + qrow * kR + ch : a.o_part + prow * kR + ch);
+          for (int h = 0; h < 2; ++h) {
+            float f[32];
+            load32(cc + h, f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+            for (int i = 0; i < 4; ++i)
+              u[4 * h + i] = make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]), pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
+                                        pack_bf16x2(f[8 * i + 4], f[8 * i + 5]), pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
+          }
+          transpose_pieces<8>(u);
+          uint16_t* dst = (uint16_t*)a.out + qrow0 * kR + col0 + 32 * cc + 8 * (lane & 7);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (row0 + i < a.rows) *reinterpret_cast<uint4*>(dst + (size_t)i * kR) = u[i];
+        }
+      } else {
+        float* base = direct ? (float*)a.out + qrow0 * kR : a.o_part + prow0 * kR;
+#pragma unroll 1
+        for (int cc = 0; cc < 8; ++cc) {
+          float f[32];
+          load32(cc, f);
+          uint4 u[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            u[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
+                              __float_as_uint(f[4 * i + 3]));
+          transpose_pieces<8>(u);
+          float* dst = base + col0 + 32 * cc + 4 * (lane & 7);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (row0 + i < a.rows) *reinterpret_cast<uint4*>(dst + (size_t)i * kR) = u[i];
         }
       }
       tc_fence_before();

@@ -399,6 +399,30 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
+// kN x kN transposition of 16-byte pieces within every group of kN lanes (kN = 4 or 8): lane m's piece i
+// becomes lane i's piece m. TMEM gives a thread one row; global memory wants a warp instruction to
+// cover whole 128-byte lines, not 16 bytes of 32 rows (32 requests in the LSU instead of 4), so rows cross
+// between a lane each (TMEM side) and kN lanes side by side (memory side) with log2(kN) exchanges.
+template <int kN>
+__device__ __forceinline__ void transpose_pieces(uint4 (&u)[kN]) {
+  const int m = threadIdx.x;
+#pragma unroll
+  for (int s = 1; s < kN; s *= 2) {
+    const bool up = (m & s) != 0;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      if (i & s) continue;
+      const uint4 give = up ? u[i] : u[i | s];
+      uint4 got;
+      got.x = __shfl_xor_sync(0xffffffffu, give.x, s);
+      got.y = __shfl_xor_sync(0xffffffffu, give.y, s);
+      got.z = __shfl_xor_sync(0xffffffffu, give.z, s);
+      got.w = __shfl_xor_sync(0xffffffffu, give.w, s);
+      if (up) u[i] = got; else u[i | s] = got;
+    }
+  }
+}
+
 // ------------------------------------------------------------------------ descriptors
 // Shared-memory matrix descriptor (sm_100 format): start address, leading and stride
 // byte offsets (all >> 4), version 1 at bits 46-47, swizzle mode at bits 61-63
