@@ -200,16 +200,20 @@ __global__ void __launch_bounds__(kThreads) simt_decode_kernel(const DecodeArgs 
 template <bool kWindow>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
   __shared__ long long s_sum[kWarps][2];
+  __shared__ int s_most[kWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.x;
   const int cap = a.len_cap;
   const auto tiles = TilesOf<kWindow>::make(a);
   // tiles before sequence b and in total, as the decode kernels' plan counts them
   long long before = 0, total = 0;
+  int most = 0, hidden = 0;
   for (int i = threadIdx.x; i < a.B; i += kThreads) {
-    const int L = __ldg(a.seq_lens + i);
-    const long long n = tiles.count(L < 0 ? 0 : (L > cap ? cap : L));
+    const int L = __ldg(a.seq_lens + i), Lc = L < 0 ? 0 : (L > cap ? cap : L);
+    const int n = tiles.count(Lc);
     total += n;
+    most = max(most, n);
+    hidden = max(hidden, tiles.gap(Lc));
     if (i < b) before += n;
   }
 #pragma unroll
@@ -217,9 +221,13 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
     before += __shfl_xor_sync(0xffffffffu, before, o);
     total += __shfl_xor_sync(0xffffffffu, total, o);
   }
+  most = __reduce_max_sync(0xffffffffu, most);
+  hidden = __reduce_max_sync(0xffffffffu, hidden);
   if (lane == 0) {
     s_sum[warp][0] = before;
     s_sum[warp][1] = total;
+    s_most[warp][0] = most;
+    s_most[warp][1] = hidden;
   }
   __syncthreads();
   before = total = 0;
@@ -227,6 +235,8 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
   for (int i = 0; i < kWarps; ++i) {
     before += s_sum[i][0];
     total += s_sum[i][1];
+    most = max(most, s_most[i][0]);
+    hidden = max(hidden, s_most[i][1]);
   }
   const int row = blockIdx.y * kWarps + warp;
   const size_t orow = (size_t)b * a.rows + row;
@@ -234,7 +244,9 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
   const float qnan = __uint_as_float(0x7FC00000u);
   const long long n = raw < 0 || raw > cap ? 0 : tiles.count(raw);
   int first = 0, splits = 0;
-  if (n > 0) {
+  if (n > 0 && tiles.whole_run(total, most, hidden, a.B, a.W)) {
+    splits = 1;
+  } else if (n > 0) {
     const int Wa = (total < a.W) ? (int)total : a.W;
     first = worker_of_tile(before, total, Wa);
     splits = worker_of_tile(before + n - 1, total, Wa) - first + 1;
