@@ -31,6 +31,44 @@ __device__ __forceinline__ float e4m3_to_float(uint32_t code) {
   return (code & 0x80) ? -v : v;
 }
 
+// A bf16 row as two e4m3 rows, so that the FP8 tensor path multiplies it: x * 2^-e = hi + lo, with one
+// e per row chosen so that its largest magnitude lands in [128, 256). A bf16 value has 8 significant bits:
+// hi is the nearest value with 4, and x - hi is a multiple of the same last place with at most 4 of its
+// own, so hi + lo is exact down to 2^-10 of the row's largest magnitude; below, lo meets e4m3's smallest
+// step (2^-9) and the error is at most 2^-10 / 128 = 2^-17 of that magnitude.
+__device__ __forceinline__ float bf16x2_amax(uint32_t v) {
+  return fmaxf(fabsf(__uint_as_float(v << 16)), fabsf(__uint_as_float(v & 0xFFFF0000u)));
+}
+// e from the row's largest magnitude (taken as at least 2^-100, so that 2^-e stays finite)
+__device__ __forceinline__ int split_exponent(float amax) { return max((int)(__float_as_uint(amax) >> 23), 27) - 127 - 7; }
+
+__device__ __forceinline__ uint32_t f32x2_to_e4m3(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+  return h;
+}
+// four values (two bf16 pairs) -> four hi codes and four lo codes; down = 2^-e
+__device__ __forceinline__ void split_e4m3(uint32_t v0, uint32_t v1, float down, uint32_t& hi, uint32_t& lo) {
+  hi = lo = 0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t w = j ? v1 : v0;
+    const float x0 = __uint_as_float(w << 16) * down, x1 = __uint_as_float(w & 0xFFFF0000u) * down;
+    const uint32_t c = f32x2_to_e4m3(x0, x1);
+    float h0, h1;
+    asm("{.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}"
+        : "=f"(h0), "=f"(h1)
+        : "r"(e4m3x2_to_half2(c)));
+    hi |= c << (16 * j);
+    lo |= f32x2_to_e4m3(x0 - h0, x1 - h1) << (16 * j);
+  }
+}
+
 __device__ __forceinline__ float load_q(const void* p, int dtype, size_t i) {
   return dtype == kF32 ? __ldg((const float*)p + i) : bf16_bits_to_float(__ldg((const uint16_t*)p + i));
 }

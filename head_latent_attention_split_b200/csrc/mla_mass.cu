@@ -16,7 +16,7 @@
 // runs of four tiles at a time (150 * 4 * 147 KB: the second group's reads hit L2); a token's sum over
 // the groups is added up by one thread, in order.
 // With an e4m3 cache the codes are an operand as they are (kind::f8f6f4): the bf16 query is split into
-// two e4m3 terms (8 = 4 + 4 significant bits, see split_row), both multiplied into one accumulator,
+// two e4m3 terms (8 = 4 + 4 significant bits, see split_e4m3), both multiplied into one accumulator,
 // and the RoPE part has its own bf16 MMAs and accumulator since the token's scale does not apply to
 // it. No conversion of cache data at all.
 // Bound: memory. Per 128 tokens and SM 36 MMAs of N = 128 take about 2.5 k cycles and the
@@ -145,49 +145,18 @@ struct MassCtl {
 };
 static_assert(sizeof(MassCtl) <= kCtlBytes, "control block");
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ void e4m3x2_to_f32(uint32_t c, float& lo, float& hi) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-  asm("{.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}" : "=f"(lo), "=f"(hi) : "r"(h));
-}
-
-// One query row (16 channels per lane, v = 8 bf16 pairs) as hi + lo e4m3 terms of x * 2^-e, 2^e chosen
-// so that the largest magnitude lands in [128, 256). A bf16 value has 8 significant bits: hi is the
-// nearest value with 4, and x - hi is a multiple of the same last place with at most 4 of its own, so
-// x = hi + lo exactly down to 2^-10 of the row's largest magnitude (below, lo meets e4m3's
-// smallest step and the error is at most 2^-10 / 128 = 2^-17 of it, 2^-18 for the nearest). Returns the
-// exponent field of 2^e.
+// One query row (16 channels per lane, v = 8 bf16 pairs) as hi + lo e4m3 terms of x * 2^-e (split_e4m3);
+// returns the exponent field of 2^e.
 __device__ __forceinline__ uint32_t split_row(const uint32_t* v, uint32_t* hi, uint32_t* lo) {
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(v[i] << 16)), fabsf(__uint_as_float(v[i] & 0xFFFF0000u))));
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, bf16x2_amax(v[i]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  // exponent field of the largest magnitude (at least 2^-100, so that 2^-e stays finite)
-  const int e = max((int)(__float_as_uint(m) >> 23), 27) - 127 - 7;
+  const int e = split_exponent(m);
   const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t h = 0, l = 0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t w = v[2 * i + j];
-      const float x0 = __uint_as_float(w << 16) * down, x1 = __uint_as_float(w & 0xFFFF0000u) * down;
-      const uint32_t c = e4m3x2(x0, x1);
-      float h0, h1;
-      e4m3x2_to_f32(c, h0, h1);
-      h |= c << (16 * j);
-      l |= e4m3x2(x0 - h0, x1 - h1) << (16 * j);
-    }
-    hi[i] = h;
-    lo[i] = l;
-  }
+  for (int i = 0; i < 4; ++i) split_e4m3(v[2 * i], v[2 * i + 1], down, hi[i], lo[i]);
   return (uint32_t)(127 + e);
 }
 

@@ -404,7 +404,7 @@ mla_status_t mla_window_decode(const mla_decode_params_t* params, int32_t window
  *
  * TCGEN05 with an E4M3 cache multiplies the codes as they are and splits each bf16 query value
  * into two e4m3 terms, x = hi + lo, scaled by a power of two per row: exact for values within
- * 2^-10 of the row's largest magnitude, off by at most 2^-18 of that magnitude below it. */
+ * 2^-10 of the row's largest magnitude, off by at most 2^-17 of that magnitude below it. */
 mla_status_t mla_attention_mass(const mla_decode_params_t* params, int32_t max_seq_len, const void* q_lat,
                                 const void* q_rope, const void* kv_cache, const void* k_rope_cache,
                                 const float* kv_scale, const int32_t* block_table, const int32_t* seq_lens,

@@ -98,8 +98,9 @@ def mass(inp, lse, mass_in):
             x = (q[b, s] @ c.T + qr[b, s] @ k.T) * w.scale
             mag = (q[b, s].abs() @ c.abs().T + qr[b, s].abs() @ k.abs().T) * abs(w.scale)
             ds = (w.r + w.d_r + 4) * U32 * mag + 2.0 ** -21 + 4 * U32 * lse[b, s][:, None].abs()
-            if w.cache_dtype == W.E4M3:   # a query value split in two e4m3 terms: 2^-18 of the row's largest
-                ds = ds + 2.0 ** -18 * abs(w.scale) * q[b, s].abs().amax(1)[:, None] * c.abs().sum(1)[None]
+            if w.cache_dtype == W.E4M3:   # a query value split in two e4m3 terms, the row's largest at 128 or more
+                # and e4m3's smallest step 2^-9, half of which is lost: 2^-10 / 128
+                ds = ds + 2.0 ** -17 * abs(w.scale) * q[b, s].abs().amax(1)[:, None] * c.abs().sum(1)[None]
             wt = torch.where(see[None], torch.exp(x - lse[b, s][:, None]), 0.0)
             res[b, :L] += wt.sum(0)
             bound[b, :L] += torch.where(see[None], wt * ds * 1.01, 0.0).sum(0)
