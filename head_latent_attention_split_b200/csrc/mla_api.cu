@@ -74,10 +74,11 @@ bool simt_ok(const mla_decode_params_t* p) {
 }
 
 // Resolve the kernel and the worker count. needs_device: the SM count was required.
+// window: the call is a window decode, whose split-role kernel takes an FP8 cache too.
 // sparse: the call is a sparse decode. AUTO then keeps the single-CTA tensor-core kernel: its
 // row gathers per tile are fewer than the split-role kernel's (which fetches each row for both
 // CTAs), and gathers bound both (measured 0.116 vs 0.158 ms for the 128K / k = 2048 step).
-mla_status_t resolve(const mla_decode_params_t* p, int* kernel, int* workers, bool sparse = false) {
+mla_status_t resolve(const mla_decode_params_t* p, int* kernel, int* workers, bool sparse = false, bool window = false) {
   mla_status_t st = check_shape(p);
   if (st) return st;
   const bool tc_ok = mla::tc_supported(p->kv_rank, p->rope_dim, p->block_size, p->q_dtype, p->cache_dtype,
@@ -87,10 +88,10 @@ mla_status_t resolve(const mla_decode_params_t* p, int* kernel, int* workers, bo
     if (!tc_ok || !mla::kTcAuto)
       k = MLA_KERNEL_SIMT;
     else
-      k = (!sparse && p->cache_dtype == MLA_DTYPE_BF16) ? MLA_KERNEL_TC_PAIR : MLA_KERNEL_TCGEN05;
+      k = window || (!sparse && p->cache_dtype == MLA_DTYPE_BF16) ? MLA_KERNEL_TC_PAIR : MLA_KERNEL_TCGEN05;
   }
   if (k == MLA_KERNEL_TCGEN05 && !tc_ok) return MLA_ERR_UNSUPPORTED;
-  if (k == MLA_KERNEL_TC_PAIR && (!tc_ok || p->cache_dtype != MLA_DTYPE_BF16)) return MLA_ERR_UNSUPPORTED;
+  if (k == MLA_KERNEL_TC_PAIR && (!tc_ok || (p->cache_dtype != MLA_DTYPE_BF16 && !window))) return MLA_ERR_UNSUPPORTED;
   if (k == MLA_KERNEL_SIMT && !simt_ok(p)) return MLA_ERR_UNSUPPORTED;
   int W = p->num_workers;
   if (W == 0) {
@@ -185,7 +186,8 @@ mla_status_t mla_decode_resolve(const mla_decode_params_t* p, int32_t* kernel, i
 mla_status_t mla_decode_workspace_size(const mla_decode_params_t* p, size_t* bytes) {
   if (!bytes) return MLA_ERR_INVALID_ARG;
   int k = 0, W = 0;
-  mla_status_t st = resolve(p, &k, &W);
+  // (window: its kernels for these parameters have the same layout and worker count, and one more of them)
+  mla_status_t st = resolve(p, &k, &W, false, true);
   if (st) return st;
   *bytes = layout_for(p, W).total;
   return MLA_OK;
@@ -198,7 +200,7 @@ mla_status_t decode_impl(const mla_decode_params_t* p, const void* q_lat, const 
                          void* workspace, size_t workspace_bytes, void* stream, void* const* events,
                          int window = 0, int sinks = 0) {
   int kernel = 0, W = 0;
-  mla_status_t st = resolve(p, &kernel, &W);
+  mla_status_t st = resolve(p, &kernel, &W, false, window > 0);
   if (st) return st;
   if (p->batch == 0) return MLA_OK;
   if (!q_lat || !kv_cache || !block_table || !seq_lens || !out || !lse) return MLA_ERR_INVALID_ARG;

@@ -34,8 +34,8 @@ __device__ __forceinline__ float e4m3_to_float(uint32_t code) {
 // A bf16 row as two e4m3 rows, so that the FP8 tensor path multiplies it: x * 2^-e = hi + lo, with one
 // e per row chosen so that its largest magnitude lands in [128, 256). A bf16 value has 8 significant bits:
 // hi is the nearest value with 4, and x - hi is a multiple of the same last place with at most 4 of its
-// own, so hi + lo is exact down to 2^-10 of the row's largest magnitude; below, lo meets e4m3's smallest
-// step (2^-9) and the error is at most 2^-10 / 128 = 2^-17 of that magnitude.
+// own, so hi + lo is exact down to 2^-10 of the row's largest magnitude; below, both meet e4m3's smallest
+// step (2^-9) and lose at most half of it each: 2^-9 / 128 = 2^-16 of that magnitude.
 __device__ __forceinline__ float bf16x2_amax(uint32_t v) {
   return fmaxf(fabsf(__uint_as_float(v << 16)), fabsf(__uint_as_float(v & 0xFFFF0000u)));
 }
@@ -47,26 +47,16 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-  return h;
-}
+// x to 4 significant bits, nearest (halves away from 0): an e4m3 value where it is not below e4m3's normal
+// range. (Integer arithmetic: conversions there and back run at a quarter of its rate or less.)
+__device__ __forceinline__ float top4(float x) { return __uint_as_float((__float_as_uint(x) + 0x80000u) & 0xFFF00000u); }
 // four values (two bf16 pairs) -> four hi codes and four lo codes; down = 2^-e
 __device__ __forceinline__ void split_e4m3(uint32_t v0, uint32_t v1, float down, uint32_t& hi, uint32_t& lo) {
-  hi = lo = 0;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const uint32_t w = j ? v1 : v0;
-    const float x0 = __uint_as_float(w << 16) * down, x1 = __uint_as_float(w & 0xFFFF0000u) * down;
-    const uint32_t c = f32x2_to_e4m3(x0, x1);
-    float h0, h1;
-    asm("{.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}"
-        : "=f"(h0), "=f"(h1)
-        : "r"(e4m3x2_to_half2(c)));
-    hi |= c << (16 * j);
-    lo |= f32x2_to_e4m3(x0 - h0, x1 - h1) << (16 * j);
-  }
+  const float x0 = __uint_as_float(v0 << 16) * down, x1 = __uint_as_float(v0 & 0xFFFF0000u) * down;
+  const float x2 = __uint_as_float(v1 << 16) * down, x3 = __uint_as_float(v1 & 0xFFFF0000u) * down;
+  const float h0 = top4(x0), h1 = top4(x1), h2 = top4(x2), h3 = top4(x3);
+  hi = f32x2_to_e4m3(h0, h1) | (f32x2_to_e4m3(h2, h3) << 16);
+  lo = f32x2_to_e4m3(x0 - h0, x1 - h1) | (f32x2_to_e4m3(x2 - h2, x3 - h3) << 16);
 }
 
 __device__ __forceinline__ float load_q(const void* p, int dtype, size_t i) {

@@ -125,7 +125,7 @@ constexpr int kQChunks = 9;                      // query: 9 x [N rows][128 byte
 constexpr int kGroupRows = 128;                  // query rows per group (at most)
 constexpr int kGroupRun = 4;                     // tiles per run when there are several groups
 // warps 0-7 sums (0-3 the even tiles, 4-7 the odd ones), 8 TMA, 9 MMA, 10-13 query split (e4m3)
-constexpr int kSumThreads = 256, kTmaWarp = 8, kMmaWarp = 9, kSplitWarp = 10;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kSplitWarp = 10;
 constexpr int kTcThreads = 32 * 14;
 constexpr uint32_t kCtlBytes = 2048;             // leaves 5 ring slots at 128 rows
 constexpr uint32_t kSmemMax = 232448;

@@ -34,6 +34,19 @@
 // kernel); pairs never straddle two sequences (a sequence with an odd number of tiles ends with
 // a single tile, scored with N = 64). Every wait is bounded; a timeout sets MLA_ERR_TIMEOUT and
 // the rows of the unfinished segments are written as NaN.
+//
+// kFp8 (window decode over an e4m3 cache): the codes are MMA operands as they are, in both CTAs; nothing
+// is converted per tile.
+//   scores: the query is split into two e4m3 terms (split_e4m3) that fill 256 TMEM columns; both multiply
+//     every 128-channel chunk of codes into one accumulator, and the RoPE parts (bf16, the query's in
+//     shared memory) have a second one, since a token's scale applies to the latent part only:
+//     score = 2^e (acc s_t + rope), the query's power of two in the row's softmax scale. 36 MMAs per tile pair,
+//     as with a bf16 cache.
+//   probabilities: P s_t as two e4m3 terms (2^-8, a bf16 rounding's accuracy), so the PV is 8 MMAs per
+//     tile on the codes themselves. The running maximum is that of score + log2 s_t, the logarithm of
+//     what P holds, and its reference sits 2^4 below it: P s_t stays in [0, 2^8], and e4m3's smallest
+//     step (2^-9, of which both terms may lose half) costs at most 2^-13 of the largest term.
+//   Half the bytes per tile: twice the ring slots.
 #include <cuda.h>
 
 #include <cmath>
@@ -57,6 +70,10 @@ constexpr uint32_t kSlotBytesS = kGroupS * kDChunk;    // 48 KB
 constexpr int kSlotsS = 3;                             // score CTA ring of slots
 constexpr uint32_t kHalf = 4 * kChunk;                 // output CTA half stage: 256 channels of a tile
 constexpr int kHalvesO = 5;                            // output CTA ring of half stages
+// e4m3 cache: slots of one chunk (128 channels of codes, or the RoPE keys, of both tiles), half stages of
+// two chunks
+constexpr int kChunksS8 = 5, kSlotsS8 = 8, kHalvesO8 = 10;
+constexpr uint32_t kSlotBytesS8 = kDChunk, kHalf8 = 2 * kChunk;
 constexpr uint32_t kPBytes = kRows * 128;              // P [128 rows][64 tokens] bf16
 constexpr uint32_t kMsgBytes = kPBytes + kRows * 8;    // + (rescale factor, 1 / row sum) per row
 constexpr int kStage = 4;                              // score CTA: outgoing message buffers
@@ -69,6 +86,15 @@ constexpr uint32_t kOffRingO = kOffRx + kRxBufs * kMsgBytes;
 constexpr uint32_t kEndS = kOffStage + kStage * kMsgBytes, kEndO = kOffRingO + kHalvesO * kHalf;
 constexpr uint32_t kOffCtl = (kEndS > kEndO ? kEndS : kEndO);
 constexpr uint32_t kSmemBytes = kOffCtl + 4096 + 1024;     // control block + alignment slack
+// e4m3 cache: the query's RoPE part [128 rows][64] bf16, then the messages; behind the control block the
+// token scales of four pairs, each softmax warp's 64 logarithms of them and 64 finite copies, the halves'
+// query maxima
+constexpr uint32_t kOffQr8 = kSlotsS8 * kSlotBytesS8, kOffStage8 = kOffQr8 + kRows * 128;
+constexpr uint32_t kOffScale8 = kOffCtl + 4096, kOffLog8 = kOffScale8 + 4 * 128 * 4, kOffQmax8 = kOffLog8 + 8 * 128 * 4;
+constexpr uint32_t kSmemBytes8 = kOffQmax8 + 2 * kRows * 4 + 1024;
+static_assert(kOffStage8 + kStage * kMsgBytes <= kOffCtl && kOffRx + kRxBufs * kMsgBytes + kHalvesO8 * kHalf8 <= kOffCtl &&
+                  kSmemBytes8 <= 232448,
+              "e4m3 layout");
 static_assert(kSlotBytesS % 1024 == 0 && kOffRingO % 1024 == 0 && kMsgBytes % 1024 == 0 && kOffCtl % 1024 == 0,
               "swizzled buffers need 1024-byte alignment");
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -79,6 +105,8 @@ constexpr uint32_t kTmemQ = 0;
 constexpr uint32_t kTmemS = 288;
 constexpr uint32_t kTmemCols = 512;
 static_assert(kTmemS + 128 <= kTmemCols, "TMEM budget of the score CTA");
+// e4m3 cache: the query's hi terms (128 columns) and lo terms (128), the latent and the RoPE scores
+constexpr uint32_t kTmemLo8 = 128, kTmemS8 = 256, kTmemR8 = 384;
 
 constexpr int kRowThreads = 256;   // warps 0-7: softmax (score CTA) / row work (output CTA)
 constexpr int kThreads = kRowThreads + 96;
@@ -86,23 +114,27 @@ constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kPostWarp = 10;      // score CTA: copies each written message to the output CTA
 constexpr float kRescaleThreshold = 8.0f;
+constexpr float kHeadroom8 = 4.0f;   // e4m3 cache: P s_t starts at 2^4 (and stays below 2^8)
+constexpr float kScaleFloor = 0x1p-64f;   // of a token's scale, in the running maximum only
 
 struct Ctl {
   // score CTA
-  uint64_t full[kSlotsS], empty[kSlotsS];
+  uint64_t full[kSlotsS8], empty[kSlotsS8];
   uint64_t q_full, q_empty;
   uint64_t s_full, s_empty;
   uint64_t written[kStage];     // the 128 softmax threads of a tile wrote its message into buffer s
   uint64_t sent[kStage];        // the message in buffer s reached the output CTA (s is free again)
   uint64_t credit[kRxBufs];     // the output CTA's PV that read receive buffer b has completed
   // output CTA
-  uint64_t ofull[kHalvesO], oempty[kHalvesO];
+  uint64_t ofull[kHalvesO8], oempty[kHalvesO8];
   uint64_t rx_full[kRxBufs];    // the message of a tile landed in receive buffer b
   uint64_t p_ready[kRxBufs];    // rows of buffer b checked (rescaled, tail zeroed): PV may run
   uint64_t pv_done[kRxBufs];
   uint64_t drain;
   uint64_t xbar[4];          // score CTA: the two softmax warps of lane quarter q posted their maxima
   uint64_t sbar[4];          // ... their row sums (a segment's last pair)
+  uint64_t qbar[4];          // ... e4m3 cache: their rows' query maxima
+  uint64_t sc_full[4];       // e4m3 cache: the token scales of pair u landed in slot u % 4
   uint32_t tmem_base;
   int abort;
   WorkerPlan plan;
@@ -166,11 +198,15 @@ __device__ __forceinline__ int sparse_row(const DecodeArgs& a, int b, int j, int
 // kWindow: the tile list holds only the blocks with sink tokens or tokens of the rows' windows
 // (WindowTiles); a row's softmax masks the tokens of those blocks that it does not see, and tokens
 // that no row sees are zeroed before the PV reads them. The pipelines are the dense ones.
-template <bool kSparse, bool kWindow>
+template <bool kSparse, bool kWindow, bool kFp8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_kv4,
+                       const __grid_constant__ CUtensorMap tm_kr, const __grid_constant__ CUtensorMap tm_sc,
                        const DecodeArgs a, const int n_rg,
                        const uint64_t timeout_ns, const uint64_t drain_ns) {
+  constexpr int kSlots = kFp8 ? kSlotsS8 : kSlotsS, kHalves = kFp8 ? kHalvesO8 : kHalvesO;
+  constexpr uint32_t kSlotBytes = kFp8 ? kSlotBytesS8 : kSlotBytesS, kHalfBytes = kFp8 ? kHalf8 : kHalf;
+  constexpr uint32_t kOffMsg = kFp8 ? kOffStage8 : kOffStage;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem + kOffCtl);
@@ -186,7 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if constexpr (kWindow) launch_dependents();   // the combine
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlotsS; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_u32(&ctl.full[i]), 1);
       mbar_init(smem_u32(&ctl.empty[i]), 1);
     }
@@ -194,7 +230,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&ctl.q_empty), 1);
     mbar_init(smem_u32(&ctl.s_full), 1);
     mbar_init(smem_u32(&ctl.s_empty), kRowThreads / 32);
-    for (int i = 0; i < kHalvesO; ++i) {
+    for (int i = 0; i < kHalves; ++i) {
       mbar_init(smem_u32(&ctl.ofull[i]), 1);
       mbar_init(smem_u32(&ctl.oempty[i]), 1);
     }
@@ -214,6 +250,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&ctl.xbar[i]), 2);
       mbar_init(smem_u32(&ctl.sbar[i]), 2);
+      mbar_init(smem_u32(&ctl.qbar[i]), 2);
+      mbar_init(smem_u32(&ctl.sc_full[i]), 1);
     }
     ctl.abort = 0;
     fence_mbarrier_init_cluster();
@@ -267,14 +305,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int m = 0; m < 4; ++m) r4[m] = act ? sparse_row(a, sg.b, tile * kBS + 4 * lane + m, sg.Lc) : 0;
 #pragma unroll 1   // rolled: see the score MMA loop
         for (int g = 0; g < kChunksS / kGroupS; ++g, ++c) {
-          const uint32_t slot = c % kSlotsS;
+          const uint32_t slot = c % kSlots;
           bool free_slot = true;
-          if (lane == 0 && c >= (uint32_t)kSlotsS)
-            free_slot = mbar_wait<false>(smem_u32(&ctl.empty[slot]), ((c / kSlotsS) & 1) ^ 1, abort, timeout_ns);
+          if (lane == 0 && c >= (uint32_t)kSlots)
+            free_slot = mbar_wait<false>(smem_u32(&ctl.empty[slot]), ((c / kSlots) & 1) ^ 1, abort, timeout_ns);
           ok = __shfl_sync(0xffffffffu, free_slot, 0);
           if (!ok) break;
           const uint32_t bar = smem_u32(&ctl.full[slot]);
-          const uint32_t dst = smem_u32(smem + kOffRingS + slot * kSlotBytesS);
+          const uint32_t dst = smem_u32(smem + kOffRingS + slot * kSlotBytes);
           if (lane == 0) mbar_arrive_expect_tx(bar, nt * kGroupS * kChunk);
           __syncwarp();
           if (act) {
@@ -287,9 +325,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) {
       int dummy = 0;
-      for (uint32_t i = 0; i < kSlotsS && i < c; ++i) {
+      for (uint32_t i = 0; i < kSlots && i < c; ++i) {
         const uint32_t cl = c - 1 - i;
-        mbar_wait<false>(smem_u32(&ctl.full[cl % kSlotsS]), (cl / kSlotsS) & 1, &dummy, drain_ns);
+        mbar_wait<false>(smem_u32(&ctl.full[cl % kSlots]), (cl / kSlots) & 1, &dummy, drain_ns);
       }
       if (!ok) set_status(a.status, MLA_ERR_TIMEOUT);
     }
@@ -300,41 +338,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // B200, the farther ahead the slower: the ring's own loads are the only reads.)
       SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
       Segment sg;
-      uint32_t c = 0;   // slots issued
+      uint32_t c = 0, u = 0, sc_issued = 0;   // slots issued, pairs, pairs whose scales are issued
       bool ok = true;
       while (ok && it.next(sg)) {
         prefetch_query(a, sg.b, rg);
-        for (int tile = sg.tile_begin; ok && tile < sg.tile_end; tile += 2) {
+        for (int tile = sg.tile_begin; ok && tile < sg.tile_end; tile += 2, ++u) {
           const int nt = min(2, sg.tile_end - tile);
           const int blk0 = tile_block(a, sg.b, tiles.block(tile, sg.Lc));
           const int blk1 = nt == 2 ? tile_block(a, sg.b, tiles.block(tile + 1, sg.Lc)) : 0;
 #pragma unroll 1   // rolled: see the score MMA loop
-          for (int g = 0; g < kChunksS / kGroupS; ++g, ++c) {
-            const uint32_t slot = c % kSlotsS;
-            if (c >= (uint32_t)kSlotsS &&
-                !mbar_wait<false>(smem_u32(&ctl.empty[slot]), ((c / kSlotsS) & 1) ^ 1, abort, timeout_ns)) {
+          for (int g = 0; g < (kFp8 ? kChunksS8 : kChunksS / kGroupS); ++g, ++c) {
+            const uint32_t slot = c % kSlots;
+            if (c >= (uint32_t)kSlots &&
+                !mbar_wait<false>(smem_u32(&ctl.empty[slot]), ((c / kSlots) & 1) ^ 1, abort, timeout_ns)) {
               ok = false;
               break;
             }
             const uint32_t bar = smem_u32(&ctl.full[slot]);
-            const uint32_t dst = smem_u32(smem + kOffRingS + slot * kSlotBytesS);
-            mbar_arrive_expect_tx(bar, nt * kGroupS * kChunk);
-            // chunk j of the pair's first tile, then of the second, for kGroupS consecutive chunks
+            const uint32_t dst = smem_u32(smem + kOffRingS + slot * kSlotBytes);
+            if constexpr (kFp8) {
+              const bool rope = g == kChunksS8 - 1;
+              mbar_arrive_expect_tx(bar, nt * kChunk);
+              for (int h = 0; h < nt; ++h)
+                tma_load_3d(dst + h * kChunk, rope ? &tm_kr : &tm_kv, bar, rope ? 0 : 128 * g, 0, h ? blk1 : blk0);
+              if (rope) {
+                // the pair's token scales, into one of four slots: this pair's MMAs cannot run before the
+                // softmax warps are done with pair u - 2, nor this load be issued before those of pair u - 2
+                const uint32_t sbar = smem_u32(&ctl.sc_full[u & 3]);
+                mbar_arrive_expect_tx(sbar, nt * kBS * 4);
+                for (int h = 0; h < nt; ++h)
+                  tma_load_3d(smem_u32(smem + kOffScale8 + (u & 3) * 512 + h * 256), &tm_sc, sbar, 0, 0, h ? blk1 : blk0);
+                ++sc_issued;
+              }
+            } else {
+              mbar_arrive_expect_tx(bar, nt * kGroupS * kChunk);
+              // chunk j of the pair's first tile, then of the second, for kGroupS consecutive chunks
 #pragma unroll
-            for (int jj = 0; jj < kGroupS; ++jj) {
-              const int j = kGroupS * g + jj;
-              tma_load_3d(dst + jj * kDChunk, &tm_kv, bar, 64 * j, 0, blk0);
-              if (nt == 2) tma_load_3d(dst + jj * kDChunk + kChunk, &tm_kv, bar, 64 * j, 0, blk1);
+              for (int jj = 0; jj < kGroupS; ++jj) {
+                const int j = kGroupS * g + jj;
+                tma_load_3d(dst + jj * kDChunk, &tm_kv, bar, 64 * j, 0, blk0);
+                if (nt == 2) tma_load_3d(dst + jj * kDChunk + kChunk, &tm_kv, bar, 64 * j, 0, blk1);
+              }
             }
           }
         }
       }
       // every load issued has landed before the CTA may exit
       int dummy = 0;
-      for (uint32_t i = 0; i < kSlotsS && i < c; ++i) {
+      for (uint32_t i = 0; i < kSlots && i < c; ++i) {
         const uint32_t cl = c - 1 - i;
-        mbar_wait<false>(smem_u32(&ctl.full[cl % kSlotsS]), (cl / kSlotsS) & 1, &dummy, drain_ns);
+        mbar_wait<false>(smem_u32(&ctl.full[cl % kSlots]), (cl / kSlots) & 1, &dummy, drain_ns);
       }
+      for (uint32_t i = sc_issued > 4 ? sc_issued - 4 : 0; kFp8 && i < sc_issued; ++i)
+        mbar_wait<false>(smem_u32(&ctl.sc_full[i & 3]), (i >> 2) & 1, &dummy, drain_ns);
       if (!ok) set_status(a.status, MLA_ERR_TIMEOUT);
     }
   } else if (rank == 0 && warp == kMmaWarp) {
@@ -342,6 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idesc2 = idesc_bf16_f32(128, 128, false);   // a tile pair
       constexpr uint32_t idesc1 = idesc_bf16_f32(128, 64, false);    // a single tile
+      constexpr uint32_t idesc2c = idesc_e4m3_f32(128, 128), idesc1c = idesc_e4m3_f32(128, 64);
       SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
       Segment sg;
       uint32_t c = 0, u = 0, seg = 0;
@@ -358,21 +415,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // Loops around barrier waits stay rolled: unrolled, the pipelines of this kernel ran about
           // 1.4x slower on B200 (measured).
 #pragma unroll 1
-          for (int g = 0; g < kChunksS / kGroupS; ++g, ++c) {
-            const uint32_t slot = c % kSlotsS;
-            ok = mbar_wait<false>(smem_u32(&ctl.full[slot]), (c / kSlotsS) & 1, abort, timeout_ns);
+          for (int g = 0; g < (kFp8 ? kChunksS8 : kChunksS / kGroupS); ++g, ++c) {
+            const uint32_t slot = c % kSlots;
+            ok = mbar_wait<false>(smem_u32(&ctl.full[slot]), (c / kSlots) & 1, abort, timeout_ns);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t base = smem_u32(smem + kOffRingS + slot * kSlotBytesS);
+            const uint32_t base = smem_u32(smem + kOffRingS + slot * kSlotBytes);
+            if constexpr (kFp8) {
+              if (g < kChunksS8 - 1) {
+                const uint32_t ic = sg.tile_end - tile >= 2 ? idesc2c : idesc1c;
 #pragma unroll
-            for (int jj = 0; jj < kGroupS; ++jj) {
-              const int j = kGroupS * g + jj;
+                for (int kk = 0; kk < 4; ++kk) {
+                  // 32 channels: eight TMEM columns of codes; hi, then lo into the same accumulator
+                  const uint64_t bdesc = smem_desc(base + kk * 32, 16, 1024, kSwizzle128B);
+                  const uint32_t qa = tmem + kTmemQ + 8 * (4 * g + kk);
+                  mma_f8_ts(tmem + kTmemS8, qa, bdesc, ic, (g | kk) ? 1u : 0u);
+                  mma_f8_ts(tmem + kTmemS8, qa + kTmemLo8, bdesc, ic, 1u);
+                }
+              } else {
+                const uint32_t qr = smem_u32(smem + kOffQr8);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                // channels [64 j + 16 kk, +16): A = query words from TMEM, B = the pair's rows of
-                // chunk j (K-major, 8-row groups 1 KB apart, the second tile right after the first)
-                const uint64_t bdesc = smem_desc(base + jj * kDChunk + kk * 32, 16, 1024, kSwizzle128B);
-                mma_ts(tmem + kTmemS, tmem + kTmemQ + 8 * (4 * j + kk), bdesc, idesc, (j | kk) ? 1u : 0u);
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_ss(tmem + kTmemR8, smem_desc(qr + kk * 32, 16, 1024, kSwizzle128B),
+                         smem_desc(base + kk * 32, 16, 1024, kSwizzle128B), idesc, kk ? 1u : 0u);
+              }
+            } else {
+#pragma unroll
+              for (int jj = 0; jj < kGroupS; ++jj) {
+                const int j = kGroupS * g + jj;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  // channels [64 j + 16 kk, +16): A = query words from TMEM, B = the pair's rows of
+                  // chunk j (K-major, 8-row groups 1 KB apart, the second tile right after the first)
+                  const uint64_t bdesc = smem_desc(base + jj * kDChunk + kk * 32, 16, 1024, kSwizzle128B);
+                  mma_ts(tmem + kTmemS, tmem + kTmemQ + 8 * (4 * j + kk), bdesc, idesc, (j | kk) ? 1u : 0u);
+                }
               }
             }
             mma_commit(smem_u32(&ctl.empty[slot]));   // the slot is free once these MMAs have read it
@@ -391,7 +468,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (rank == 0 && warp < kProducerWarp) {
     // ------------------------------------------------------------------ score CTA: softmax warps
-    const float scale_log2 = a.scale_log2;
     SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
     Segment sg;
     uint32_t t = 0, u = 0, seg = 0;   // tiles and pairs before this segment, segments
@@ -400,6 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int n = sg.tile_end - sg.tile_begin;
       float m_run = -INFINITY, l_run = 0.f, l_tot = 0.f;   // l_run: this half's columns
       bool poisoned = false;
+      float scale_log2 = a.scale_log2;   // e4m3 cache: times 2^e, the power of two of this row's query
       if (ok) {
         // this segment's absorbed query into TMEM: of every row, half 0 loads the latent channels
         // [0, 256), half 1 the channels [256, 512) and the RoPE channels
@@ -411,7 +488,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int row0 = rg * kRows + 32 * quarter + (lane & ~7);   // query row of this lane group's first row
           const uint16_t* ql = (const uint16_t*)a.q_lat + ((size_t)sg.b * a.rows + row0) * kR + 256 * half + 8 * (lane & 7);
           const uint16_t* qr = (const uint16_t*)a.q_rope + ((size_t)sg.b * a.rows + row0) * kDR + 8 * (lane & 7);
-          const int nb = half ? 5 : 4;   // half 1 loads the RoPE channels too
           auto fetch = [&](int k, uint4 (&q)[8]) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -419,15 +495,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                          ? __ldg(reinterpret_cast<const uint4*>(k < 4 ? ql + (size_t)i * kR + 64 * k : qr + (size_t)i * kDR))
                          : make_uint4(0u, 0u, 0u, 0u);
           };
-          uint4 qv[2][8];
-          fetch(0, qv[0]);
+          // blocks in the order RoPE (k = 4; half 1 only), latent 0 .. 3, two of them on their way: block k is
+          // number i0 = (k + 1) % 5
+          uint4 n0[8], n1[8];
+          auto start = [&] {
+            if (half == 1) {
+              fetch(4, n0);
+              fetch(0, n1);
+            } else {
+              fetch(0, n0);
+              fetch(1, n1);
+            }
+          };
+          auto step = [&](int i0, uint4 (&q)[8]) {
 #pragma unroll
-          for (int k = 0; k < 5; ++k) {
-            if (k >= nb) break;
-            if (k + 1 < nb) fetch(k + 1, qv[(k + 1) & 1]);
-            uint4 (&q)[8] = qv[k & 1];
-            transpose_pieces<8>(q);
-            uint32_t w32[32];
+            for (int i = 0; i < 8; ++i) {
+              q[i] = n0[i];
+              n0[i] = n1[i];
+            }
+            if (i0 + 2 < 5) fetch(i0 + 1, n1);
+          };
+          auto words = [&](const uint4 (&q)[8], uint32_t (&w32)[32]) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               w32[4 * i] = q[i].x;
@@ -435,8 +523,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               w32[4 * i + 2] = q[i].z;
               w32[4 * i + 3] = q[i].w;
             }
-            // column = word index of the absorbed query row
-            tmem_st32(tmem + lane_off + kTmemQ + (k < 4 ? 128 * half + 32 * k : 256), w32);
+          };
+          if constexpr (kFp8) {
+            // The rows' largest magnitudes: over this half's channels (piece by piece of eight rows, then across
+            // the eight lanes that share them), then with the other half's.
+            float mx[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mx[i] = 0.f;
+            {
+              uint4 q[4][8];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) fetch(k, q[k]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  mx[i] = fmaxf(mx[i], fmaxf(fmaxf(bf16x2_amax(q[k][i].x), bf16x2_amax(q[k][i].y)),
+                                             fmaxf(bf16x2_amax(q[k][i].z), bf16x2_amax(q[k][i].w))));
+            }
+            start();
+            if (half == 1) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                mx[i] = fmaxf(mx[i], fmaxf(fmaxf(bf16x2_amax(n0[i].x), bf16x2_amax(n0[i].y)),
+                                           fmaxf(bf16x2_amax(n0[i].z), bf16x2_amax(n0[i].w))));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int o = 1; o < 8; o *= 2) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+            float m = mx[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) m = (lane & 7) == i ? mx[i] : m;   // row 8 (lane / 8) + lane % 8: this lane's
+            float* qmax = reinterpret_cast<float*>(smem + kOffQmax8);
+            qmax[half * kRows + row] = m;
+            warp_arrive(smem_u32(&ctl.qbar[quarter]));
+            ok = wait_warp(smem_u32(&ctl.qbar[quarter]), seg & 1);
+            const int e = split_exponent(fmaxf(m, qmax[(half ^ 1) * kRows + row]));
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            scale_log2 = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll 1
+            for (int i0 = half ? 0 : 1; i0 < 5; ++i0) {
+              const int k = (i0 + 4) % 5;
+              uint4 q[8];
+              uint32_t w32[32];
+              step(i0, q);
+              transpose_pieces<8>(q);
+              words(q, w32);
+              if (k < 4) {   // 64 channels as 16 words of hi codes and 16 of lo
+                uint32_t hl[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) split_e4m3(w32[2 * i], w32[2 * i + 1], down, hl[i], hl[16 + i]);
+                tmem_st16(tmem + lane_off + kTmemQ + 64 * half + 16 * k, hl);
+                tmem_st16(tmem + lane_off + kTmemQ + kTmemLo8 + 64 * half + 16 * k, hl + 16);
+              } else {       // RoPE channels, scaled alike: 128 bytes of the K-major operand, 128-byte swizzle
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  w32[i] = pack_bf16x2(__uint_as_float(w32[i] << 16) * down, __uint_as_float(w32[i] & 0xFFFF0000u) * down);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  *reinterpret_cast<uint4*>(smem + kOffQr8 + row * 128 + ((i ^ (row & 7)) << 4)) =
+                      make_uint4(w32[4 * i], w32[4 * i + 1], w32[4 * i + 2], w32[4 * i + 3]);
+                fence_proxy_async_smem();
+              }
+            }
+          } else {
+            start();
+#pragma unroll 1   // rolled: code that runs once per segment waits for its instructions
+            for (int i0 = half ? 0 : 1; i0 < 5; ++i0) {
+              const int k = (i0 + 4) % 5;
+              uint4 q[8];
+              uint32_t w32[32];
+              step(i0, q);
+              transpose_pieces<8>(q);
+              words(q, w32);
+              // column = word index of the absorbed query row
+              tmem_st32(tmem + lane_off + kTmemQ + (k < 4 ? 128 * half + 32 * k : 256), w32);
+            }
           }
           tmem_wait_st();
           tc_fence_before();
@@ -455,11 +618,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           uint32_t v[64];
-          tmem_ld32(tmem + lane_off + kTmemS + 64 * half, v);
-          tmem_ld32(tmem + lane_off + kTmemS + 64 * half + 32, v + 32);
+          constexpr uint32_t kScores = kFp8 ? kTmemS8 : kTmemS;
+          tmem_ld32(tmem + lane_off + kScores + 64 * half, v);
+          tmem_ld32(tmem + lane_off + kScores + 64 * half + 32, v + 32);
+          uint32_t r[kFp8 ? 64 : 1];   // e4m3 cache: the RoPE scores
+          if constexpr (kFp8) {
+            tmem_ld32(tmem + lane_off + kTmemR8 + 64 * half, r);
+            tmem_ld32(tmem + lane_off + kTmemR8 + 64 * half + 32, r + 32);
+          }
           tmem_wait_ld();
           tc_fence_before();
           warp_arrive(smem_u32(&ctl.s_empty));
+          // e4m3 cache: the tile's token scales, and this warp's copy of their logarithms and of themselves
+          const float* sc = reinterpret_cast<const float*>(smem + kOffScale8) + (u & 3) * 128 + 64 * half;
+          float* lsc = reinterpret_cast<float*>(smem + kOffLog8) + warp * 128;
+          if constexpr (kFp8) {
+            ok = wait_warp(smem_u32(&ctl.sc_full[u & 3]), (u >> 2) & 1);
+            if (!ok) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float s = sc[lane + 32 * h];
+              lsc[lane + 32 * h] = __log2f(fmaxf(s, kScaleFloor));
+              // (behind p = 0 of a token that is not seen, whose scale may be anything)
+              lsc[64 + lane + 32 * h] = fabsf(s) < INFINITY ? s : 0.f;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 64; j += 4) {
+              const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(sc + j);
+#pragma unroll
+              for (int i = 0; i < 4; i += 2) {
+                const unsigned long long x =
+                    fma2(f2_pack(__uint_as_float(v[j + i]), __uint_as_float(v[j + i + 1])), i ? s4.y : s4.x,
+                         f2_pack(__uint_as_float(r[j + i]), __uint_as_float(r[j + i + 1])));
+                float x0, x1;
+                f2_unpack(x, x0, x1);
+                v[j + i] = __float_as_uint(x0);
+                v[j + i + 1] = __float_as_uint(x1);
+              }
+            }
+          }
           // The pair's row maximum of the scaled scores (log2 units) from both halves. A full tile
           // keeps the raw scores and takes the extreme with three-input min / max (the scale folds
           // into the exponent's FMA below); a partial one masks the columns past the row's
@@ -468,7 +666,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const WindowCols cols(a, mine ? n_row : 0, kWindow ? tiles.block(tile, sg.Lc) * kBS : 0, kBS);
           const bool full = kWindow ? cols.all(kBS) : valid == kBS;
           float mh;
-          if (full) {
+          if (kFp8) {   // the maximum of score + log2 of the token's scale
+            mh = -INFINITY;
+            const float c = full ? scale_log2 : 1.f;
+            if (!full) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                v[j] = __float_as_uint(cols.sees(j) ? __uint_as_float(v[j]) * scale_log2 : -INFINITY);
+            }
+            const unsigned long long c2 = f2_pack(c, c);
+#pragma unroll
+            for (int j = 0; j < 64; j += 4) {
+              const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(lsc + j);
+#pragma unroll
+              for (int i = 0; i < 4; i += 2) {
+                float t0, t1;
+                f2_unpack(fma2(f2_pack(__uint_as_float(v[j + i]), __uint_as_float(v[j + i + 1])), c2, i ? l4.y : l4.x), t0, t1);
+                mh = max3f(mh, t0, t1);
+              }
+            }
+          } else if (full) {
             float r = __uint_as_float(v[0]);
             if (scale_log2 >= 0.f) {
 #pragma unroll
@@ -496,10 +713,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!ok) break;
           const float mt = fmaxf(mh, ctl.xmax[u & 1][half ^ 1][row]);
           const bool grow_max = mt > m_run + kRescaleThreshold;
-          const float alpha = (grow_max && m_run != -INFINITY) ? ex2_approx(m_run - mt) : 1.f;
+          const float m_new = kFp8 ? mt - kHeadroom8 : mt;
+          const float alpha = (grow_max && m_run != -INFINITY) ? ex2_approx(m_run - m_new) : 1.f;
           if (grow_max) {
             l_run *= alpha;
-            m_run = mt;
+            m_run = m_new;
           }
           uint32_t pk[32];
           float psum = 0.f;
@@ -508,8 +726,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float c = full ? scale_log2 : 1.f;
             const unsigned long long cc = f2_pack(c, c), nm = f2_pack(-m_run, -m_run);
             unsigned long long acc = f2_pack(0.f, 0.f);
+            if constexpr (kFp8) {
+              // four columns at a time: p, its sum, and p s_t as one word of hi and one of lo codes
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
+              for (int k = 0; k < 16; ++k) {
+                const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(lsc + 64 + 4 * k);
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int j = 4 * k + 2 * h;
+                  float x0, x1, w0, w1, l0, l1;
+                  f2_unpack(fma2(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), cc, nm), x0, x1);
+                  const unsigned long long p2 = f2_pack(ex2_approx(x0), ex2_approx(x1));
+                  acc = add2(acc, p2);
+                  const unsigned long long w2 = mul2(p2, h ? s4.y : s4.x);
+                  f2_unpack(w2, w0, w1);
+                  const float h0 = top4(w0), h1 = top4(w1);
+                  f2_unpack(fma2(f2_pack(h0, h1), f2_pack(-1.f, -1.f), w2), l0, l1);
+                  hi[h] = f32x2_to_e4m3(h0, h1);
+                  lo[h] = f32x2_to_e4m3(l0, l1);
+                }
+                pk[k] = hi[0] | (hi[1] << 16);
+                pk[16 + k] = lo[0] | (lo[1] << 16);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < (kFp8 ? 0 : 32); ++k) {
               float x0, x1;
               f2_unpack(fma2(f2_pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), cc, nm), x0, x1);
               const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
@@ -547,7 +789,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // this row of the tile's message: P as [8-token chunk][row][8 tokens] (8-row x 16-byte
             // core matrices, the K-major layout the output CTA's PV reads), then the row's
             // (rescale factor, 1 / row sum)
-            uint8_t* msg = smem + kOffStage + sb * kMsgBytes;
+            uint8_t* msg = smem + kOffMsg + sb * kMsgBytes;
 #pragma unroll
             for (int cc = 0; cc < 8; ++cc)
               *reinterpret_cast<uint4*>(msg + cc * (kRows * 16) + row * 16) =
@@ -589,7 +831,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = mbar_wait<true>(smem_u32(&ctl.credit[rb]), ((t / kRxBufs) & 1) ^ 1, abort, timeout_ns);
           if (!ok) break;
           bulk_copy_to_peer(mapa(smem_u32(smem + kOffRx + rb * kMsgBytes), peer),
-                            smem_u32(smem + kOffStage + sb * kMsgBytes), kMsgBytes,
+                            smem_u32(smem + kOffMsg + sb * kMsgBytes), kMsgBytes,
                             mapa(smem_u32(&ctl.rx_full[rb]), peer));
         }
       }
@@ -618,15 +860,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int m = 0; m < 4; ++m) r4[m] = act ? sparse_row(a, sg.b, tile * kBS + 4 * lane + m, sg.Lc) : 0;
 #pragma unroll 1   // rolled: see the score MMA loop
         for (int hc = 0; hc < 2; ++hc, ++h) {
-          const uint32_t hs = h % kHalvesO;
+          const uint32_t hs = h % kHalves;
           bool free_half = true;
-          if (lane == 0 && h >= (uint32_t)kHalvesO)
-            free_half = mbar_wait<false>(smem_u32(&ctl.oempty[hs]), ((h / kHalvesO) & 1) ^ 1, abort, timeout_ns);
+          if (lane == 0 && h >= (uint32_t)kHalves)
+            free_half = mbar_wait<false>(smem_u32(&ctl.oempty[hs]), ((h / kHalves) & 1) ^ 1, abort, timeout_ns);
           ok = __shfl_sync(0xffffffffu, free_half, 0);
           if (!ok) break;
           const uint32_t bar = smem_u32(&ctl.ofull[hs]);
-          const uint32_t base = smem_u32(smem + kOffRingO + hs * kHalf);
-          if (lane == 0) mbar_arrive_expect_tx(bar, kHalf);
+          const uint32_t base = smem_u32(smem + kOffRingO + hs * kHalfBytes);
+          if (lane == 0) mbar_arrive_expect_tx(bar, kHalfBytes);
           __syncwarp();
           if (act) {
 #pragma unroll
@@ -638,9 +880,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) {
       int dummy = 0;
-      for (uint32_t i = 0; i < kHalvesO && i < h; ++i) {
+      for (uint32_t i = 0; i < kHalves && i < h; ++i) {
         const uint32_t hl = h - 1 - i;
-        mbar_wait<false>(smem_u32(&ctl.ofull[hl % kHalvesO]), (hl / kHalvesO) & 1, &dummy, drain_ns);
+        mbar_wait<false>(smem_u32(&ctl.ofull[hl % kHalves]), (hl / kHalves) & 1, &dummy, drain_ns);
       }
       if (!ok) set_status(a.status, MLA_ERR_TIMEOUT);
     }
@@ -656,30 +898,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int blk = tile_block(a, sg.b, tiles.block(tile, sg.Lc));
 #pragma unroll 1   // rolled: see the score MMA loop
           for (int hc = 0; hc < 2; ++hc, ++h) {
-            const uint32_t hs = h % kHalvesO;
-            if (h >= (uint32_t)kHalvesO &&
-                !mbar_wait<false>(smem_u32(&ctl.oempty[hs]), ((h / kHalvesO) & 1) ^ 1, abort, timeout_ns)) {
+            const uint32_t hs = h % kHalves;
+            if (h >= (uint32_t)kHalves &&
+                !mbar_wait<false>(smem_u32(&ctl.oempty[hs]), ((h / kHalves) & 1) ^ 1, abort, timeout_ns)) {
               ok = false;
               break;
             }
             const uint32_t bar = smem_u32(&ctl.ofull[hs]);
-            const uint32_t base = smem_u32(smem + kOffRingO + hs * kHalf);
-            mbar_arrive_expect_tx(bar, kHalf);
-            tma_load_4d(base, &tm_kv4, bar, 0, 0, 4 * hc, blk);   // latent chunks 4 hc .. 4 hc + 3
+            const uint32_t base = smem_u32(smem + kOffRingO + hs * kHalfBytes);
+            mbar_arrive_expect_tx(bar, kHalfBytes);
+            tma_load_4d(base, &tm_kv4, bar, 0, 0, (kFp8 ? 2 : 4) * hc, blk);   // latent chunks of 256 channels
           }
         }
       }
       int dummy = 0;
-      for (uint32_t i = 0; i < kHalvesO && i < h; ++i) {
+      for (uint32_t i = 0; i < kHalves && i < h; ++i) {
         const uint32_t hl = h - 1 - i;
-        mbar_wait<false>(smem_u32(&ctl.ofull[hl % kHalvesO]), (hl / kHalvesO) & 1, &dummy, drain_ns);
+        mbar_wait<false>(smem_u32(&ctl.ofull[hl % kHalves]), (hl / kHalves) & 1, &dummy, drain_ns);
       }
       if (!ok) set_status(a.status, MLA_ERR_TIMEOUT);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ output CTA: MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 256, true);
+      constexpr uint32_t idesc_pv = kFp8 ? idesc_e4m3_f32(128, 256, true) : idesc_bf16_f32(128, 256, true);
       const uint32_t rx = smem_u32(smem + kOffRx);
       SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
       Segment sg;
@@ -694,11 +936,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_after();
 #pragma unroll 1   // rolled: see the score MMA loop
           for (int hc = 0; hc < 2; ++hc, ++h) {
-            const uint32_t hs = h % kHalvesO;
-            ok = mbar_wait<false>(smem_u32(&ctl.ofull[hs]), (h / kHalvesO) & 1, abort, timeout_ns);
+            const uint32_t hs = h % kHalves;
+            ok = mbar_wait<false>(smem_u32(&ctl.ofull[hs]), (h / kHalves) & 1, abort, timeout_ns);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t base = smem_u32(smem + kOffRingO + hs * kHalf);
+            const uint32_t base = smem_u32(smem + kOffRingO + hs * kHalfBytes);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               // A = P[128 rows][tokens 16 kk .. +16] (K-major); B = C[16 tokens][256 channels],
@@ -706,8 +948,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               // (the message's P: 8-row x 16-byte core matrices, 128 bytes apart along the rows,
               // 2 KB apart along the tokens)
               const uint64_t adesc = smem_desc(rx + rb * kMsgBytes + kk * 4096, 2048, 128, kSwizzleNone);
-              const uint64_t bdesc = smem_desc(base + kk * 2048, kChunk, 1024, kSwizzle128B);
-              mma_ss(tmem + 256 * hc, adesc, bdesc, idesc_pv, (li > 0 || kk > 0) ? 1u : 0u);
+              // e4m3 cache: k-steps of 32 tokens, the hi terms of P (chunks of 16 tokens 0-3 of the message)
+              // in the first two and the lo terms (4-7) in the others; 128-channel chunks
+              const uint64_t bdesc = smem_desc(base + (kFp8 ? (kk & 1) * 4096 : kk * 2048), kChunk, 1024, kSwizzle128B);
+              if constexpr (kFp8)
+                mma_f8_ss(tmem + 256 * hc, adesc, bdesc, idesc_pv, (li > 0 || kk > 0) ? 1u : 0u);
+              else
+                mma_ss(tmem + 256 * hc, adesc, bdesc, idesc_pv, (li > 0 || kk > 0) ? 1u : 0u);
             }
             mma_commit(smem_u32(&ctl.oempty[hs]));
           }
@@ -781,16 +1028,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int first = max(min(max(tiles.lo(sg.Lc) - base, 0), kBS), sink), end = min(sg.Lc - base, kBS);
             if (sink < first || end < kBS) {
               const uint32_t h0 = 2 * t, h1 = 2 * t + 1;
-              ok = wait_warp(smem_u32(&ctl.ofull[h0 % kHalvesO]), (h0 / kHalvesO) & 1) &&
-                   wait_warp(smem_u32(&ctl.ofull[h1 % kHalvesO]), (h1 / kHalvesO) & 1);
+              ok = wait_warp(smem_u32(&ctl.ofull[h0 % kHalves]), (h0 / kHalves) & 1) &&
+                   wait_warp(smem_u32(&ctl.ofull[h1 % kHalves]), (h1 / kHalves) & 1);
               if (!ok) break;
               const int from = min(first, end);   // rows to zero: [sink, from) and [end, 64)
               const int hole = from - sink, gone = hole + (kBS - end);
-              for (int i = threadIdx.x; i < 64 * gone; i += kRowThreads) {
-                const int ck = i & 7, pc = (i >> 3) & 7, k = i >> 6;
+              constexpr int kCk = kFp8 ? 4 : 8;   // 128-byte chunks of a token's row
+              for (int i = threadIdx.x; i < 8 * kCk * gone; i += kRowThreads) {
+                const int ck = i % kCk, pc = (i / kCk) & 7, k = i / (8 * kCk);
                 const int tok = k < hole ? sink + k : end + (k - hole);
-                const uint32_t hs = (ck < 4 ? h0 : h1) % kHalvesO;
-                *reinterpret_cast<uint4*>(smem + kOffRingO + hs * kHalf + (ck & 3) * kChunk + tok * 128 + pc * 16) =
+                const uint32_t hs = (ck < kCk / 2 ? h0 : h1) % kHalves;
+                *reinterpret_cast<uint4*>(smem + kOffRingO + hs * kHalfBytes + (ck % (kCk / 2)) * kChunk + tok * 128 + pc * 16) =
                     make_uint4(0u, 0u, 0u, 0u);
               }
               fence_proxy_async_smem();
@@ -799,14 +1047,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // cache slots past the sequence end may hold anything (NaN): zero those token rows
             // of both half stages before the PV reads them (P is 0 there, but 0 * NaN is not)
             const uint32_t h0 = 2 * t, h1 = 2 * t + 1;
-            ok = wait_warp(smem_u32(&ctl.ofull[h0 % kHalvesO]), (h0 / kHalvesO) & 1) &&
-                 wait_warp(smem_u32(&ctl.ofull[h1 % kHalvesO]), (h1 / kHalvesO) & 1);
+            ok = wait_warp(smem_u32(&ctl.ofull[h0 % kHalves]), (h0 / kHalves) & 1) &&
+                 wait_warp(smem_u32(&ctl.ofull[h1 % kHalves]), (h1 / kHalves) & 1);
             if (!ok) break;
             const int per_chunk = (kBS - tail) * 8;   // 16-byte pieces per chunk
             for (int i = threadIdx.x; i < 8 * per_chunk; i += kRowThreads) {
               const int ck = i / per_chunk, rem = i % per_chunk;
-              const uint32_t hs = (ck < 4 ? h0 : h1) % kHalvesO;
-              uint8_t* p = smem + kOffRingO + hs * kHalf + (ck & 3) * kChunk + (tail + rem / 8) * 128 + (rem % 8) * 16;
+              const uint32_t hs = (ck < 4 ? h0 : h1) % kHalves;
+              uint8_t* p = smem + kOffRingO + hs * kHalfBytes + (ck & 3) * kChunk + (tail + rem / 8) * 128 + (rem % 8) * 16;
               *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
@@ -911,8 +1159,31 @@ cudaError_t launch_pair_decode(const DecodeArgs& a, cudaStream_t s) {
   if (!fn) return cudaErrorInvalidValue;
   const bool sparse = a.sel_idx != nullptr;
   if (sparse && (a.Sq != 1 || a.causal)) return cudaErrorInvalidValue;
-  CUtensorMap tm, tm4;
-  if (sparse) {
+  const bool windowed = a.window > 0, fp8 = a.cache_dtype == kE4M3;
+  if (sparse && windowed) return cudaErrorInvalidValue;
+  if (fp8 && !windowed) return cudaErrorInvalidValue;
+  CUtensorMap tm, tm4, tmr, tms;
+  auto encode = [&](CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                    const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, type, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (fp8) {
+    const cuuint64_t nb = (cuuint64_t)a.num_blocks;
+    // codes [num_blocks][64][512], boxes of 128 channels x 64 tokens; the same as (128 channels, 64
+    // tokens, 4 chunks, blocks), boxes of two chunks; RoPE keys [num_blocks][64][64] bf16; scales
+    const cuuint64_t d3[3] = {kR, kBS, nb}, s3[2] = {kR, (cuuint64_t)kBS * kR};
+    const cuuint64_t d4[4] = {128, kBS, kR / 128, nb}, s4[3] = {kR, 128, (cuuint64_t)kBS * kR};
+    const cuuint64_t dr[3] = {kDR, kBS, nb}, sr[2] = {kDR * 2, (cuuint64_t)kBS * kDR * 2};
+    const cuuint64_t ds[3] = {kBS, 1, nb}, ss[2] = {kBS * 4, kBS * 4};
+    const cuuint32_t b3[3] = {128, kBS, 1}, b4[4] = {128, kBS, 2, 1}, br[3] = {kDR, kBS, 1}, bs[3] = {kBS, 1, 1};
+    if (!encode(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.cache, d3, s3, b3, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode(&tm4, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a.cache, d4, s4, b4, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode(&tmr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.k_rope, dr, sr, br, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode(&tms, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, a.kv_scale, ds, ss, bs, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return cudaErrorInvalidValue;
+  } else if (sparse) {
     // the cache as rows [num_blocks * 64][576] bf16: one-row boxes of 64 channels (128 bytes,
     // 128-byte swizzle) for 4-row gathers; rows past the cache read as zeros
     const cuuint64_t dims[2] = {(cuuint64_t)(kR + kDR), (cuuint64_t)a.num_blocks * kBS};
@@ -945,22 +1216,22 @@ cudaError_t launch_pair_decode(const DecodeArgs& a, cudaStream_t s) {
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  const bool windowed = a.window > 0;
-  if (sparse && windowed) return cudaErrorInvalidValue;
-  auto kernel = sparse     ? pair_decode_kernel<true, false>
-                : windowed ? pair_decode_kernel<false, true>
-                           : pair_decode_kernel<false, false>;
-  static std::once_flag attr_once[3][64];
+  if (!fp8) tmr = tms = tm;   // unused by the bf16 kernels
+  auto kernel = sparse     ? pair_decode_kernel<true, false, false>
+                : fp8      ? pair_decode_kernel<false, true, true>
+                : windowed ? pair_decode_kernel<false, true, false>
+                           : pair_decode_kernel<false, false, false>;
+  const int smem = fp8 ? kSmemBytes8 : kSmemBytes;
+  static std::once_flag attr_once[4][64];
   int dev = 0;
   cudaGetDevice(&dev);
   cudaError_t attr_err = cudaSuccess;
-  std::call_once(attr_once[sparse ? 1 : windowed ? 2 : 0][dev & 63], [&] {
-    attr_err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  });
+  std::call_once(attr_once[sparse ? 1 : fp8 ? 3 : windowed ? 2 : 0][dev & 63],
+                 [&] { attr_err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (attr_err != cudaSuccess) return attr_err;
   const int n_rg = (a.rows + kRows - 1) / kRows;
   const dim3 grid(2 * a.W * n_rg);
-  kernel<<<grid, kThreads, kSmemBytes, s>>>(tm, tm4, a, n_rg, wait_timeout_ns(), drain_timeout_ns());
+  kernel<<<grid, kThreads, smem, s>>>(tm, tm4, tmr, tms, a, n_rg, wait_timeout_ns(), drain_timeout_ns());
   return cudaGetLastError();
 }
 

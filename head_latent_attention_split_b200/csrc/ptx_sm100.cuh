@@ -339,6 +339,16 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// The same with A from TMEM (four codes per 32-bit column).
+__device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                : "memory");
@@ -484,12 +494,13 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, boo
          | ((M >> 4) << 24);
 }
 
-// Instruction descriptor for kind::f8f6f4 with e4m3 A/B (format code 0), both K-major,
-// fp32 accumulation.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
+// Instruction descriptor for kind::f8f6f4 with e4m3 A/B (format code 0), A K-major, fp32
+// accumulation.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, bool b_mn_major = false) {
   return (1u << 4)                   // D format: f32
          | (0u << 7)                 // A format: e4m3
          | (0u << 10)                // B format: e4m3
+         | ((b_mn_major ? 1u : 0u) << 16)
          | ((N >> 3) << 17)
          | ((M >> 4) << 24);
 }

@@ -376,9 +376,11 @@ mla_status_t mla_sparse_decode(const mla_decode_params_t* params, int32_t top_k,
  * so a row's window holds its last `window` tokens, its own included, and a sink inside the window
  * counts once. window >= 1, sinks >= 0; values past the block table's capacity act as the
  * capacity (a window of at least the sequence's length is mla_decode). out, lse, the other
- * arguments, the workspace (mla_decode_workspace_size of the same params), the kernels and the
- * handling of bad lengths and blocks are mla_decode's; the sequences' RoPE keys keep the
- * positions they were rotated for. Blocks that hold no token any row sees are not read and
+ * arguments, the workspace (mla_decode_workspace_size of the same params) and the handling of
+ * bad lengths and blocks are mla_decode's; the sequences' RoPE keys keep the positions they were
+ * rotated for. Kernels: mla_decode's, and MLA_KERNEL_TC_PAIR takes an E4M3 cache too (AUTO's choice
+ * for it): the query and the weights then go to the FP8 tensor path as two e4m3 terms each, the query's
+ * error at most 2^-16 of its row's largest magnitude (RoPE part included), a weight's 2^-8 as with a bf16 cache. Blocks that hold no token any row sees are not read and
  * their block ids are not checked. Tokens that no row of the sequence sees may hold anything (NaN
  * included); a token that some row sees has to be finite, as in mla_decode. */
 mla_status_t mla_window_decode(const mla_decode_params_t* params, int32_t window, int32_t sinks,
@@ -404,7 +406,7 @@ mla_status_t mla_window_decode(const mla_decode_params_t* params, int32_t window
  *
  * TCGEN05 with an E4M3 cache multiplies the codes as they are and splits each bf16 query value
  * into two e4m3 terms, x = hi + lo, scaled by a power of two per row: exact for values within
- * 2^-10 of the row's largest magnitude, off by at most 2^-17 of that magnitude below it. */
+ * 2^-10 of the row's largest magnitude, off by at most 2^-16 of that magnitude below it. */
 mla_status_t mla_attention_mass(const mla_decode_params_t* params, int32_t max_seq_len, const void* q_lat,
                                 const void* q_rope, const void* kv_cache, const void* k_rope_cache,
                                 const float* kv_scale, const int32_t* block_table, const int32_t* seq_lens,

@@ -33,6 +33,14 @@ def rows_of(inp, b, n):
     return x[:, :w.r], x[:, w.r:]
 
 
+def scales_of(inp, b, n):
+    """fp8 cache: the scales of the first n tokens of sequence b, float64."""
+    w = inp["workload"]
+    t = np.arange(n)
+    slot = inp["block_table"][b, t // w.block_size].astype(np.int64) * w.block_size + t % w.block_size
+    return to64(inp["kv_scale"].reshape(-1)[slot], W.F32)
+
+
 def tokens_of_row(w, L, s):
     return max(L - w.Sq + 1 + s if w.causal else L, 0)
 
@@ -68,15 +76,23 @@ def window(inp, win, sinks):
             # a score: D products summed in fp32, and the scale's own rounding; 2^x to 2 units in the
             # last place; an fp8 key's RoPE part is held as two bf16 terms (2^-16)
             ds = (D + 4) * U32 * mag.amax(1) + 2.0 ** -21
-            if w.cache_dtype == W.E4M3:
-                ds = ds + 2.0 ** -16 * mag.amax(1)
+            if w.cache_dtype == W.E4M3:   # ... or the query as two e4m3 terms, see mass()
+                ds = ds + 2.0 ** -16 * mag.amax(1) + 2.0 ** -16 * abs(w.scale) * torch.maximum(
+                    q[b, s].abs().amax(1), qr[b, s].abs().amax(1)) * c.abs().sum(1).amax()
             n = x.shape[1]
             bl[b, s] = ds + (n + 8) * U32 + 4 * U32 * lse[b, s].abs()
-            # out: the weights' errors, their rounding for the second product (bf16; fp16 with an
-            # fp8 cache, whose smallest step is 2^-24), its sum in fp32, and the output's rounding
-            up = {W.F32: 0.0, W.BF16: UBF, W.E4M3: U16}[w.cache_dtype]
+            # out: the weights' errors, their rounding for the second product, its sum in fp32, and the
+            # output's rounding. The weights go in as bf16; with an fp8 cache as weight * scale s, in two
+            # e4m3 terms: 2^-4 of what the first leaves, which is 2^-4 again (or in fp16: 2^-11). At
+            # e4m3's smallest step 2^-9 each term may lose half of it, 2^-9 per token and code of at most
+            # 448, where the largest weight * s is at least 2^4 (its logarithm t is the softmax's maximum).
+            up = {W.F32: 0.0, W.BF16: UBF, W.E4M3: 2.0 ** -8}[w.cache_dtype]
             bo[b, s] = ac * (2 * ds[:, None] + up + (n + 8) * U32)
             if w.cache_dtype == W.E4M3:
+                t = x + torch.log(scales_of(inp, b, L)[see].clamp(min=2.0 ** -64))
+                z = torch.exp(x - t.amax(1, keepdim=True)).sum(1, keepdim=True)
+                bo[b, s] += 2.0 ** -9 * 448 / 16 * n / z
+                # (the kernel that keeps them in fp16: its smallest step, 2^-24)
                 z = torch.exp(x - x.amax(1, keepdim=True)).sum(1, keepdim=True)
                 bo[b, s] += 2.0 ** -25 * 448 * n / z
             if w.out_dtype == W.BF16:
@@ -99,8 +115,8 @@ def mass(inp, lse, mass_in):
             mag = (q[b, s].abs() @ c.abs().T + qr[b, s].abs() @ k.abs().T) * abs(w.scale)
             ds = (w.r + w.d_r + 4) * U32 * mag + 2.0 ** -21 + 4 * U32 * lse[b, s][:, None].abs()
             if w.cache_dtype == W.E4M3:   # a query value split in two e4m3 terms, the row's largest at 128 or more
-                # and e4m3's smallest step 2^-9, half of which is lost: 2^-10 / 128
-                ds = ds + 2.0 ** -17 * abs(w.scale) * q[b, s].abs().amax(1)[:, None] * c.abs().sum(1)[None]
+                # and e4m3's smallest step 2^-9, of which each term may lose half: 2^-9 / 128
+                ds = ds + 2.0 ** -16 * abs(w.scale) * q[b, s].abs().amax(1)[:, None] * c.abs().sum(1)[None]
             wt = torch.where(see[None], torch.exp(x - lse[b, s][:, None]), 0.0)
             res[b, :L] += wt.sum(0)
             bound[b, :L] += torch.where(see[None], wt * ds * 1.01, 0.0).sum(0)

@@ -80,6 +80,11 @@ CASES = [
     (FP8.with_(B=4, seq_lens=(1, 63, 1000, 450)), "auto", 100, 4, 0),
     (FP8.with_(B=3, Sq=2, H=32, causal=True, seq_lens=(1, 700, 129)), "auto", 64, 70, 5),
     (FP8.with_(B=2, seq_lens=(300, 90)), "simt", 40, 2, 0),
+    (FP8.with_(B=4, seq_lens=(1, 63, 1000, 450)), "tcgen05", 100, 4, 0),
+    (FP8.with_(B=3, Sq=2, H=80, causal=True, seq_lens=(2, 1500, 129)), "tc_pair", 700, 70, 3),
+    (FP8.with_(B=2, seq_lens=(300, 500), zero_every=7, tiny_every=5), "auto", 200, 3, 0),
+    (FP8.with_(B=2, seq_lens=(300, 500), tiny_every=2, tiny_exp=-18, out_dtype=W.F32), "auto", 200, 3, 2),
+    (FP8.with_(B=2, seq_lens=(300, 500), zero_every=1), "auto", 200, 3, 0),
 ]
 
 
@@ -107,7 +112,8 @@ def test_a_window_over_everything_is_the_decode(w):
     ref = mla.decode(t["q_lat"], t["q_rope"], t["kv_cache"], t["block_table"], t["seq_lens"], w.scale, w.causal,
                      t["k_rope_cache"], t["kv_scale"])
     for win, sinks in ((int(max(inp["seq_lens"])), 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1)):
-        out, lse, st = run(inp, win, sinks)
+        # (an e4m3 cache's decode runs the channel-split kernel, its window decode the split-role one)
+        out, lse, st = run(inp, win, sinks, kernel="tcgen05" if w.cache_dtype == W.E4M3 else "auto")
         assert st == 0 and torch.equal(out, ref[0]) and torch.equal(lse, ref[1]), (win, sinks)
 
 
