@@ -116,13 +116,14 @@ struct WindowTiles {
   __device__ __forceinline__ int block(int i, int Lc) const { return i < sink_tiles(Lc) ? i : i + gap(Lc); }
   // Sequences per worker when each worker takes whole sequences, 0 when the tile list is cut evenly.
   // A window's tile lists are short and nearly all alike, so whole sequences are often almost as even, and
-  // they cost no partial outputs and nothing to merge (about 10 tiles' time) and, unless a worker's
-  // even share is a tile or two, one segment's start and end less (about 6). Worth it while the longest
-  // share exceeds the even one by less (64 sequences of 65 tiles on 74 workers: 129 us cut evenly, 112 us
-  // whole). Where nothing is hidden the cut stays the dense one, and with it the result.
+  // they cost no partial outputs, nothing to merge and fewer segments per worker. Worth it while the
+  // longest share exceeds the even one by no more tiles than that saves, as measured on 74 workers, 128
+  // rows, bf16 (even cut, whole): 64 sequences of 65 tiles 129, 111 us; 40 of 33 77, 70; 8 of 33 54, 60;
+  // two per worker: 80 of 8 67, 57; 80 of 17 80, 81; a tile or less per worker: 8 of 8 40, 33.
+  // Where nothing is hidden the cut stays the dense one, and with it the result.
   __device__ __forceinline__ int whole_run(long long T, int most, int hidden, int B, int W) const {
-    const int k = (B + W - 1) / W;
-    return whole && hidden > 0 && (long long)k * most <= T / W + (T > 2 * W ? 16 : 10) ? k : 0;
+    const int k = (B + W - 1) / W, more = T <= 2 * W ? 12 : k == 1 ? 22 : 16;
+    return whole && hidden > 0 && (long long)k * most <= T / W + more ? k : 0;
   }
 };
 
