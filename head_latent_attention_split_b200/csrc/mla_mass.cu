@@ -130,6 +130,11 @@ constexpr int kTcThreads = 32 * 14;
 constexpr uint32_t kCtlBytes = 2048;             // leaves 5 ring slots at 128 rows
 constexpr uint32_t kSmemMax = 232448;
 
+// What the producer tells the MMA warp about a tile, released by the tile's first chunk. The producer is
+// ahead of it by the ring at most (12 chunks: two tiles and a part), so eight slots do.
+constexpr int kTileFlags = 8;
+enum : uint32_t { kFirst = 1, kLast = 2, kStop = 4 };   // tile of an item; no more tiles
+
 struct MassCtl {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t q_full[kQChunks], q_empty[kQChunks];   // e4m3: [0] the split latent part, [8] the RoPE part
@@ -141,6 +146,7 @@ struct MassCtl {
   alignas(16) float nl2[kGroupRows];   // -lse * log2(e) of the group's rows; -inf for rows that are none
   alignas(16) float a2[kGroupRows];    // e4m3: the row's power of two * scale * log2(e)
   uint8_t late[kGroupRows];  // causal: query tokens between the group's first row and this one
+  uint32_t flags[kTileFlags];
   uint8_t pow2[kGroupRows];  // e4m3: exponent field of the row's power of two (split warps -> sum warps)
 };
 static_assert(sizeof(MassCtl) <= kCtlBytes, "control block");
@@ -237,7 +243,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ---------------------------------------------------------------- TMA producer
     if (lane == 0) {
       int slot = 0, issued = 0;
-      uint32_t phase = 0, item = 0, q_issued = 0;   // query chunks loaded so far
+      uint32_t phase = 0, item = 0, u = 0, q_issued = 0;   // u: tiles; q_issued: query chunks loaded so far
       const bool ok = for_items([&](int b, int Lc, int g, int t0, int t1) {
         const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
         const int blocks = tiles_of(Lc, kBS);
@@ -264,6 +270,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               ++q_issued;
             }
             if (!mbar_wait<false>(smem_u32(&ctl.empty[slot]), phase ^ 1, abort, timeout_ns)) return false;
+            if (j == 0) ctl.flags[u++ % kTileFlags] = (t == t0 ? kFirst : 0u) | (t == t1 - 1 ? kLast : 0u);
             const uint32_t bar = smem_u32(&ctl.full[slot]);
             mbar_arrive_expect_tx(bar, nblk * kBox);
             for (int h = 0; h < nblk; ++h) {
@@ -287,9 +294,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ++item;
         return true;
       });
-      // every load issued lands before the CTA may exit
+      // the end, in place of a tile's first chunk
+      const bool stop = ok && mbar_wait<false>(smem_u32(&ctl.empty[slot]), phase ^ 1, abort, timeout_ns);
+      if (stop) {
+        ctl.flags[u % kTileFlags] = kStop;
+        mbar_arrive(smem_u32(&ctl.full[slot]));
+      }
+      // every load issued lands before the CTA may exit (the one that was in the end's slot has)
       int dummy = 0;
-      for (int i = max(0, issued - slots); i < issued; ++i)
+      for (int i = max(0, issued - slots + (stop ? 1 : 0)); i < issued; ++i)
         mbar_wait<false>(smem_u32(&ctl.full[i % slots]), (i / slots) & 1, &dummy, drain_ns);
       if (!ok) {   // the query chunks of an unfinished item too
         constexpr uint32_t per = kFp8 ? 1 : kQChunks;
@@ -299,59 +312,66 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
   } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc16 = idesc_bf16_f32(kTile, N, false), idesc8 = idesc_e4m3_f32(kTile, N);
-      int slot = 0;
-      uint32_t phase = 0, item = 0, u = 0;
-      const bool ok = for_items([&](int, int, int, int t0, int t1) {
-        for (int t = t0; t < t1; ++t, ++u) {
-          if (!mbar_wait<false>(smem_u32(&ctl.acc_empty[u & 1]), ((u >> 1) & 1) ^ 1, abort, timeout_ns)) return false;
-          const uint32_t d = tmem + (u & 1) * kAccCols;
+    // ---------------------------------------------------------------- MMA issuer (a converged warp)
+    const bool leader = elect_one();
+    const uint32_t idesc16 = idesc_bf16_f32(kTile, N, false), idesc8 = idesc_e4m3_f32(kTile, N);
+    // operand descriptors of ring slot 0 and query chunk 0; a step of 32 bytes (K = 16 bf16 or 32 codes) adds 2
+    const uint64_t ring_desc = smem_desc(sRing, 16, 1024, kSwizzle128B), q_desc = smem_desc(sQ, 16, 1024, kSwizzle128B);
+    auto wait = [&](uint64_t& bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait<false>(smem_u32(&bar), parity, abort, timeout_ns));
+    };
+    int slot = 0;
+    uint32_t phase = 0, item = 0, u = 0;
+    bool ok;
+    while ((ok = wait(ctl.full[slot], phase))) {   // the tile's first chunk, or the end
+      const uint32_t flags = __shfl_sync(0xffffffffu, ctl.flags[u % kTileFlags], 0);
+      if (flags & kStop) break;
+      ok = wait(ctl.acc_empty[u & 1], ((u >> 1) & 1) ^ 1);
+      const uint32_t d = tmem + (u & 1) * kAccCols;
 #pragma unroll 1
-          for (int j = 0; j < kChunks; ++j) {
-            const bool rope = j == kChunks - 1;
-            const int qj = kFp8 ? (rope ? kQChunks - 1 : 0) : j;   // the barrier of this chunk's query
-            if (t == t0 && !mbar_wait<false>(smem_u32(&ctl.q_full[qj]), item & 1, abort, timeout_ns)) return false;
-            if (!mbar_wait<false>(smem_u32(&ctl.full[slot]), phase, abort, timeout_ns)) return false;
-            tc_fence_after();
-            const uint32_t ka = sRing + slot * kSlot;
-            if (kFp8 && !rope) {
+      for (int j = 0; ok && j < kChunks; ++j) {
+        const bool rope = j == kChunks - 1;
+        const int qj = kFp8 ? (rope ? kQChunks - 1 : 0) : j;   // the barrier of this chunk's query
+        if (flags & kFirst) ok = wait(ctl.q_full[qj], item & 1);
+        if (ok && j > 0) ok = wait(ctl.full[slot], phase);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t ad = ring_desc + (uint32_t)slot * (kSlot >> 4);
+        const uint64_t bd = q_desc + (uint32_t)(rope ? kQChunks - 1 : j) * (q_chunk >> 4);
+        if (leader) {
+          if (kFp8 && !rope) {
+            const uint64_t lo = bd + 4 * (q_chunk >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                // 32 codes = 32 bytes of every 128-byte row; hi then lo into the same accumulator
-                const uint64_t ad = smem_desc(ka + kk * 32, 16, 1024, kSwizzle128B);
-                mma_f8_ss(d, ad, smem_desc(sQ + j * q_chunk + kk * 32, 16, 1024, kSwizzle128B), idesc8, (j | kk) ? 1u : 0u);
-                mma_f8_ss(d, ad, smem_desc(sQ + (4 + j) * q_chunk + kk * 32, 16, 1024, kSwizzle128B), idesc8, 1u);
-              }
-            } else {
-              const uint32_t qb = sQ + (rope ? kQChunks - 1 : j) * q_chunk;
-              const uint32_t dd = kFp8 ? d + kGroupRows : d;   // e4m3: RoPE scores in their own columns
+            for (int kk = 0; kk < 4; ++kk) {   // hi then lo into the same accumulator
+              mma_f8_ss(d, ad + 2 * kk, bd + 2 * kk, idesc8, (j | kk) ? 1u : 0u);
+              mma_f8_ss(d, ad + 2 * kk, lo + 2 * kk, idesc8, 1u);
+            }
+          } else {
+            const uint32_t dd = kFp8 ? d + kGroupRows : d;   // e4m3: RoPE scores in their own columns
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ss(dd, smem_desc(ka + kk * 32, 16, 1024, kSwizzle128B), smem_desc(qb + kk * 32, 16, 1024, kSwizzle128B),
-                       idesc16, (kFp8 ? kk : j | kk) ? 1u : 0u);
-            }
-            mma_commit(smem_u32(&ctl.empty[slot]));
-            if (t == t1 - 1 && (!kFp8 || rope)) {   // the query's chunk is free (e4m3: all of it) for the next item
-              mma_commit(smem_u32(&ctl.q_empty[rope ? kQChunks - 1 : j]));
-              if (kFp8) mma_commit(smem_u32(&ctl.q_empty[0]));
-            }
-            if (++slot == slots) {
-              slot = 0;
-              phase ^= 1;
-            }
+            for (int kk = 0; kk < 4; ++kk) mma_ss(dd, ad + 2 * kk, bd + 2 * kk, idesc16, (kFp8 ? kk : j | kk) ? 1u : 0u);
           }
-          mma_commit(smem_u32(&ctl.acc_full[u & 1]));
+          mma_commit(smem_u32(&ctl.empty[slot]));
+          if ((flags & kLast) && (!kFp8 || rope)) {   // the query's chunk is free (e4m3: all of it) for the next item
+            mma_commit(smem_u32(&ctl.q_empty[rope ? kQChunks - 1 : j]));
+            if (kFp8) mma_commit(smem_u32(&ctl.q_empty[0]));
+          }
+          if (rope) mma_commit(smem_u32(&ctl.acc_full[u & 1]));
         }
-        ++item;
-        return true;
-      });
-      int dummy = 0;
-      mma_commit(smem_u32(&ctl.drain));
-      mbar_wait<false>(smem_u32(&ctl.drain), 0, &dummy, drain_ns);
-      if (!ok) set_status(a.status, MLA_ERR_TIMEOUT);
+        if (++slot == slots) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      if (flags & kLast) ++item;
+      ++u;
     }
+    int dummy = 0;
+    if (leader) mma_commit(smem_u32(&ctl.drain));
+    __syncwarp();
+    mbar_wait<false>(smem_u32(&ctl.drain), 0, &dummy, drain_ns);
+    if (!ok && lane == 0) set_status(a.status, MLA_ERR_TIMEOUT);
   } else if (warp >= kSplitWarp) {
     // ---------------------------------------------------------------- e4m3: the query in two terms
     if constexpr (kFp8) {
