@@ -395,77 +395,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (rank == 0 && warp == kMmaWarp) {
     // ------------------------------------------------------------------ score CTA: MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc2 = idesc_bf16_f32(128, 128, false);   // a tile pair
-      constexpr uint32_t idesc1 = idesc_bf16_f32(128, 64, false);    // a single tile
-      constexpr uint32_t idesc2c = idesc_e4m3_f32(128, 128), idesc1c = idesc_e4m3_f32(128, 64);
-      SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
-      Segment sg;
-      uint32_t c = 0, u = 0, seg = 0;
-      bool ok = true;
-      while (ok && it.next(sg)) {
-        ok = mbar_wait<false>(smem_u32(&ctl.q_full), seg & 1, abort, timeout_ns);
+    // The whole warp walks and waits, converged, and one elected lane issues (see elect_one): the score
+    // MMAs are the kernel's critical path, and a single-lane branch computed and moved their operands one
+    // by one (windows of 64 sequences x 65 tiles: 108 us, 101 us like this).
+    const bool leader = elect_one();
+    constexpr uint32_t idesc2 = idesc_bf16_f32(128, 128, false);   // a tile pair
+    constexpr uint32_t idesc1 = idesc_bf16_f32(128, 64, false);    // a single tile
+    constexpr uint32_t idesc2c = idesc_e4m3_f32(128, 128), idesc1c = idesc_e4m3_f32(128, 64);
+    // descriptor of ring slot 0's rows (K-major, 8-row groups 1 KB apart, the second tile right after the
+    // first); 32 bytes along K add 2
+    const uint64_t ring_desc = smem_desc(smem_u32(smem + kOffRingS), 16, 1024, kSwizzle128B);
+    const uint64_t qr_desc = smem_desc(smem_u32(smem + kOffQr8), 16, 1024, kSwizzle128B);
+    SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
+    Segment sg;
+    uint32_t slot = 0, phase = 0, u = 0, seg = 0;
+    bool ok = true;
+    while (ok && __any_sync(0xffffffffu, it.next(sg))) {
+      const int tile_begin = __shfl_sync(0xffffffffu, sg.tile_begin, 0), tile_end = __shfl_sync(0xffffffffu, sg.tile_end, 0);
+      ok = wait_warp(smem_u32(&ctl.q_full), seg & 1);
+      if (!ok) break;
+      tc_fence_after();
+      for (int tile = tile_begin; ok && tile < tile_end; tile += 2, ++u) {
+        const bool two = tile_end - tile >= 2;
+        if (u >= 1) ok = wait_warp(smem_u32(&ctl.s_empty), (u & 1) ^ 1);
         if (!ok) break;
         tc_fence_after();
-        for (int tile = sg.tile_begin; ok && tile < sg.tile_end; tile += 2, ++u) {
-          const uint32_t idesc = sg.tile_end - tile >= 2 ? idesc2 : idesc1;
-          if (u >= 1) ok = mbar_wait<false>(smem_u32(&ctl.s_empty), (u & 1) ^ 1, abort, timeout_ns);
+        // Loops around barrier waits stay rolled: unrolled, the pipelines of this kernel ran about
+        // 1.4x slower on B200 (measured).
+#pragma unroll 1
+        for (int g = 0; g < (kFp8 ? kChunksS8 : kChunksS / kGroupS); ++g) {
+          ok = wait_warp(smem_u32(&ctl.full[slot]), phase);
           if (!ok) break;
           tc_fence_after();
-          // Loops around barrier waits stay rolled: unrolled, the pipelines of this kernel ran about
-          // 1.4x slower on B200 (measured).
-#pragma unroll 1
-          for (int g = 0; g < (kFp8 ? kChunksS8 : kChunksS / kGroupS); ++g, ++c) {
-            const uint32_t slot = c % kSlots;
-            ok = mbar_wait<false>(smem_u32(&ctl.full[slot]), (c / kSlots) & 1, abort, timeout_ns);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t base = smem_u32(smem + kOffRingS + slot * kSlotBytes);
+          const uint64_t bdesc = ring_desc + slot * (kSlotBytes >> 4);
+          if (leader) {
             if constexpr (kFp8) {
               if (g < kChunksS8 - 1) {
-                const uint32_t ic = sg.tile_end - tile >= 2 ? idesc2c : idesc1c;
+                // 32 channels per step: eight TMEM columns of codes; hi, then lo into the same accumulator
+                const uint32_t qa = tmem + kTmemQ + 32 * g, ic = two ? idesc2c : idesc1c;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                  // 32 channels: eight TMEM columns of codes; hi, then lo into the same accumulator
-                  const uint64_t bdesc = smem_desc(base + kk * 32, 16, 1024, kSwizzle128B);
-                  const uint32_t qa = tmem + kTmemQ + 8 * (4 * g + kk);
-                  mma_f8_ts(tmem + kTmemS8, qa, bdesc, ic, (g | kk) ? 1u : 0u);
-                  mma_f8_ts(tmem + kTmemS8, qa + kTmemLo8, bdesc, ic, 1u);
+                  mma_f8_ts(tmem + kTmemS8, qa + 8 * kk, bdesc + 2 * kk, ic, (g | kk) ? 1u : 0u);
+                  mma_f8_ts(tmem + kTmemS8, qa + kTmemLo8 + 8 * kk, bdesc + 2 * kk, ic, 1u);
                 }
               } else {
-                const uint32_t qr = smem_u32(smem + kOffQr8);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                  mma_ss(tmem + kTmemR8, smem_desc(qr + kk * 32, 16, 1024, kSwizzle128B),
-                         smem_desc(base + kk * 32, 16, 1024, kSwizzle128B), idesc, kk ? 1u : 0u);
+                  mma_ss(tmem + kTmemR8, qr_desc + 2 * kk, bdesc + 2 * kk, two ? idesc2 : idesc1, kk ? 1u : 0u);
               }
             } else {
+              const uint32_t qa = tmem + kTmemQ + 8 * 4 * kGroupS * g;
 #pragma unroll
               for (int jj = 0; jj < kGroupS; ++jj) {
-                const int j = kGroupS * g + jj;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                  // channels [64 j + 16 kk, +16): A = query words from TMEM, B = the pair's rows of
-                  // chunk j (K-major, 8-row groups 1 KB apart, the second tile right after the first)
-                  const uint64_t bdesc = smem_desc(base + jj * kDChunk + kk * 32, 16, 1024, kSwizzle128B);
-                  mma_ts(tmem + kTmemS, tmem + kTmemQ + 8 * (4 * j + kk), bdesc, idesc, (j | kk) ? 1u : 0u);
+                  // 16 channels per step: A = query words from TMEM, B = the pair's rows of chunk kGroupS g + jj
+                  mma_ts(tmem + kTmemS, qa + 8 * (4 * jj + kk), bdesc + jj * (kDChunk >> 4) + 2 * kk, two ? idesc2 : idesc1,
+                         (g | jj | kk) ? 1u : 0u);
                 }
               }
             }
             mma_commit(smem_u32(&ctl.empty[slot]));   // the slot is free once these MMAs have read it
           }
-          if (!ok) break;
-          mma_commit(smem_u32(&ctl.s_full));
+          if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
         if (!ok) break;
-        mma_commit(smem_u32(&ctl.q_empty));
-        ++seg;
+        if (leader) mma_commit(smem_u32(&ctl.s_full));
       }
-      int dummy = 0;
-      mma_commit(smem_u32(&ctl.drain));
-      mbar_wait<false>(smem_u32(&ctl.drain), 0, &dummy, drain_ns);
-      if (!ok) set_status(a.status, MLA_ERR_TIMEOUT);
+      if (!ok) break;
+      if (leader) mma_commit(smem_u32(&ctl.q_empty));
+      ++seg;
     }
+    int dummy = 0;
+    if (leader) mma_commit(smem_u32(&ctl.drain));
+    __syncwarp();
+    mbar_wait<false>(smem_u32(&ctl.drain), 0, &dummy, drain_ns);
+    if (!ok && lane == 0) set_status(a.status, MLA_ERR_TIMEOUT);
   } else if (rank == 0 && warp < kProducerWarp) {
     // ------------------------------------------------------------------ score CTA: softmax warps
     SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
@@ -919,56 +927,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!ok) set_status(a.status, MLA_ERR_TIMEOUT);
     }
   } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ output CTA: MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_pv = kFp8 ? idesc_e4m3_f32(128, 256, true) : idesc_bf16_f32(128, 256, true);
-      const uint32_t rx = smem_u32(smem + kOffRx);
-      SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
-      Segment sg;
-      uint32_t t = 0, h = 0;
-      bool ok = true;
-      while (ok && it.next(sg)) {
-        const int n = sg.tile_end - sg.tile_begin;
-        for (int li = 0; li < n; ++li, ++t) {
-          const uint32_t rb = t % kRxBufs;
-          ok = mbar_wait<false>(smem_u32(&ctl.p_ready[rb]), (t / kRxBufs) & 1, abort, timeout_ns);
+    // ------------------------------------------------------------------ output CTA: MMA issuer (converged warp)
+    const bool leader = elect_one();
+    constexpr uint32_t idesc_pv = kFp8 ? idesc_e4m3_f32(128, 256, true) : idesc_bf16_f32(128, 256, true);
+    // A = P[128 rows][16 tokens per step] (K-major); the message's P: 8-row x 16-byte core matrices, 128
+    // bytes apart along the rows, 2 KB apart along the tokens
+    const uint64_t rx_desc = smem_desc(smem_u32(smem + kOffRx), 2048, 128, kSwizzleNone);
+    // B = C[16 tokens][256 channels], channels contiguous: 64-channel chunks 8 KB apart, 8-token groups 1 KB
+    // apart. e4m3 cache: steps of 32 tokens, the hi terms of P (chunks of 16 tokens 0-3 of the message) in
+    // the first two and the lo terms (4-7) in the others; 128-channel chunks
+    const uint64_t ring_desc = smem_desc(smem_u32(smem + kOffRingO), kChunk, 1024, kSwizzle128B);
+    SegIter it(plan, a.seq_lens, a.B, tiles, cap, w, a.status);
+    Segment sg;
+    uint32_t rb = 0, rx_phase = 0, hs = 0, phase = 0;
+    bool ok = true;
+    while (ok && __any_sync(0xffffffffu, it.next(sg))) {
+      const int n = __shfl_sync(0xffffffffu, sg.tile_end - sg.tile_begin, 0);
+      for (int li = 0; li < n; ++li) {
+        ok = wait_warp(smem_u32(&ctl.p_ready[rb]), rx_phase);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1   // rolled: see the score MMA loop
+        for (int hc = 0; hc < 2; ++hc) {
+          ok = wait_warp(smem_u32(&ctl.ofull[hs]), phase);
           if (!ok) break;
           tc_fence_after();
-#pragma unroll 1   // rolled: see the score MMA loop
-          for (int hc = 0; hc < 2; ++hc, ++h) {
-            const uint32_t hs = h % kHalves;
-            ok = mbar_wait<false>(smem_u32(&ctl.ofull[hs]), (h / kHalves) & 1, abort, timeout_ns);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t base = smem_u32(smem + kOffRingO + hs * kHalfBytes);
+          const uint64_t adesc = rx_desc + rb * (kMsgBytes >> 4), bdesc = ring_desc + hs * (kHalfBytes >> 4);
+          if (leader) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              // A = P[128 rows][tokens 16 kk .. +16] (K-major); B = C[16 tokens][256 channels],
-              // channels contiguous: 64-channel chunks 8 KB apart, 8-token groups 1 KB apart
-              // (the message's P: 8-row x 16-byte core matrices, 128 bytes apart along the rows,
-              // 2 KB apart along the tokens)
-              const uint64_t adesc = smem_desc(rx + rb * kMsgBytes + kk * 4096, 2048, 128, kSwizzleNone);
-              // e4m3 cache: k-steps of 32 tokens, the hi terms of P (chunks of 16 tokens 0-3 of the message)
-              // in the first two and the lo terms (4-7) in the others; 128-channel chunks
-              const uint64_t bdesc = smem_desc(base + (kFp8 ? (kk & 1) * 4096 : kk * 2048), kChunk, 1024, kSwizzle128B);
+              const uint32_t acc = (li > 0 || kk > 0) ? 1u : 0u;
               if constexpr (kFp8)
-                mma_f8_ss(tmem + 256 * hc, adesc, bdesc, idesc_pv, (li > 0 || kk > 0) ? 1u : 0u);
+                mma_f8_ss(tmem + 256 * hc, adesc + kk * (4096 >> 4), bdesc + (kk & 1) * (4096 >> 4), idesc_pv, acc);
               else
-                mma_ss(tmem + 256 * hc, adesc, bdesc, idesc_pv, (li > 0 || kk > 0) ? 1u : 0u);
+                mma_ss(tmem + 256 * hc, adesc + kk * (4096 >> 4), bdesc + kk * (2048 >> 4), idesc_pv, acc);
             }
             mma_commit(smem_u32(&ctl.oempty[hs]));
           }
-          if (!ok) break;
+          if (++hs == kHalves) {
+            hs = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (leader) {
           mma_commit(smem_u32(&ctl.pv_done[rb]));   // O is free again after this PV
           // the receive buffer goes back to the score CTA when this PV has completed
           mma_commit_to_ctas(smem_u32(&ctl.credit[rb]), (uint16_t)(1u << peer));
         }
+        if (++rb == kRxBufs) {
+          rb = 0;
+          rx_phase ^= 1;
+        }
       }
-      int dummy = 0;
-      mma_commit(smem_u32(&ctl.drain));
-      mbar_wait<false>(smem_u32(&ctl.drain), 0, &dummy, drain_ns);
-      if (!ok) set_status(a.status, MLA_ERR_TIMEOUT);
     }
+    int dummy = 0;
+    if (leader) mma_commit(smem_u32(&ctl.drain));
+    __syncwarp();
+    mbar_wait<false>(smem_u32(&ctl.drain), 0, &dummy, drain_ns);
+    if (!ok && lane == 0) set_status(a.status, MLA_ERR_TIMEOUT);
   } else if (warp < kProducerWarp) {
     // ------------------------------------------------------------------ output CTA: row warps
     // thread = row; warp q works on O columns [0, 256) of its rows, warp q + 4 on [256, 512)
