@@ -588,18 +588,18 @@ cudaError_t launch_mass_tc(const MassArgs& m0, cudaStream_t s) {
   if (!fp8) tkr = tkv;   // unused
   auto kernel = fp8 ? mass_tc_kernel<true> : mass_tc_kernel<false>;
   static std::once_flag once[2][64];
-  static int sms[64];
+  static int sms[2][64];
   int dev = 0;
   cudaGetDevice(&dev);
   cudaError_t err = cudaSuccess;
   std::call_once(once[fp8 ? 1 : 0][dev & 63], [&] {
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms[dev & 63], cudaDevAttrMultiProcessorCount, dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms[fp8 ? 1 : 0][dev & 63], cudaDevAttrMultiProcessorCount, dev);
   });
   if (err != cudaSuccess) return err;
   // one CTA per SM, fewer when there cannot be as many tiles
   const long long most = (long long)a.B * ((a.len_cap + kTile - 1) / kTile);
-  if (m.d.W == 0) m.d.W = (int)std::min<long long>(std::max(sms[dev & 63], 1), std::max(most, 1ll));
+  if (m.d.W == 0) m.d.W = (int)std::min<long long>(std::max(sms[fp8 ? 1 : 0][dev & 63], 1), std::max(most, 1ll));
   kernel<<<m.d.W, kTcThreads, smem, s>>>(tq, tqr, tkv, tkr, m, N, slots, wait_timeout_ns(), drain_timeout_ns());
   return cudaGetLastError();
 }

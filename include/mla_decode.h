@@ -397,12 +397,15 @@ mla_status_t mla_window_decode(const mla_decode_params_t* params, int32_t window
  *                                exp(sigma_t(s,h) - lse[b,s,h]),        t < seq_lens[b],
  *
  * with mla_decode's scores, causal rule and lse output (so each row adds 1 over the sequence). All
- * sums are fp32, in a fixed order. mass_in may be NULL (zeros) or equal mass; entries
- * t >= seq_lens[b] are not written. mass_in, mass f32 [B, max_seq_len]; lse f32 [B, Sq, H].
+ * sums are fp32, in a fixed order. mass_in may be NULL (zeros) or equal mass (no other overlap);
+ * entries t >= seq_lens[b] are not written. The caller keeps the entries of positions without a
+ * token at 0, so that a token appended there starts without weight: after a verification that
+ * shortens a sequence, set the refused drafts' entries to 0. mass_in, mass f32 [B, max_seq_len]; lse f32 [B, Sq, H].
  * params: as for mla_decode (out_dtype is not used; kernel AUTO, SIMT or TCGEN05; num_workers
  * is the number of CTAs of the TCGEN05 kernel, 0 = one per SM). A seq_len above max_seq_len
  * or the block table's capacity sets MLA_ERR_BAD_SEQ_LEN and skips the sequence; tokens of a
- * block id out of range get NaN and set MLA_ERR_BAD_BLOCK_ID. Asynchronous, allocates nothing.
+ * block id out of range get NaN and set MLA_ERR_BAD_BLOCK_ID; tokens not finished when a wait runs
+ * out (MLA_ERR_TIMEOUT) get NaN. Asynchronous, allocates nothing.
  *
  * TCGEN05 with an E4M3 cache multiplies the codes as they are and splits each bf16 query value
  * into two e4m3 terms, x = hi + lo, scaled by a power of two per row: exact for values within
@@ -443,8 +446,8 @@ mla_status_t mla_evict_select(const mla_evict_params_t* params, const float* mas
  * sequences may share one. The copies run in no particular order.
  * Cache tensors and dtypes as in mla_decode; indices int32 [B, list_stride]; counts outside
  * [0, list_stride] are clamped and set MLA_ERR_BAD_SEQ_LEN; an entry whose position or block is
- * out of range is not copied, its mass becomes NaN, and MLA_ERR_BAD_BLOCK_ID is set.
- * Asynchronous, allocates nothing. */
+ * out of range is not copied, its mass becomes NaN, and MLA_ERR_BAD_BLOCK_ID is set. After
+ * MLA_ERR_TIMEOUT some entries have not been copied. Asynchronous, allocates nothing. */
 typedef struct {
   int32_t batch;            /* B */
   int32_t kv_rank;          /* r */

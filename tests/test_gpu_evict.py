@@ -180,3 +180,63 @@ def test_front_end_refuses_tensors_that_do_not_fit():
         mla.cache_compact(kv, bt, dt, idx, cnt.long())
     torch.cuda.synchronize()
     assert mla.device_status() == 0
+
+
+def test_an_expired_wait_ends_cleanly():
+    import torch
+    import head_latent_attention_split_b200 as mla
+    B, bs, n = 40, 64, 40
+    kv = torch.randn(2 * B * 8, bs, 576, device="cuda").bfloat16()
+    old = kv.clone()
+    i32 = lambda x: x.to(torch.int32).cuda()  # noqa: E731
+    bt, dt = i32(torch.arange(B * 8).reshape(B, 8)), i32(torch.arange(B * 8, 2 * B * 8).reshape(B, 8))
+    idx, cnt = i32(torch.arange(0, 8 * bs, 2)[None].expand(B, -1)).contiguous(), i32(torch.full((B,), 4 * bs))
+    mla.set_wait_timeout_ns(1)
+    try:
+        mla.cache_compact(kv, bt, dt, idx, cnt)
+        torch.cuda.synchronize()
+    finally:
+        mla.set_wait_timeout_ns(0)
+    assert mla.device_status() in (0, 8) and mla.device_status() == 0
+    assert torch.equal(kv[:B * 8], old[:B * 8])          # the sources are never written
+    mla.cache_compact(kv, bt, dt, idx, cnt)
+    torch.cuda.synchronize()
+    assert mla.device_status() == 0
+    rows = lambda x: x.reshape(B, 8 * bs, 576)  # noqa: E731
+    assert torch.equal(rows(kv[B * 8:])[:, :4 * bs], rows(kv[:B * 8])[:, ::2][:, :4 * bs])
+    assert torch.equal(rows(kv[B * 8:])[:, 4 * bs:], rows(old[B * 8:])[:, 4 * bs:])
+
+
+def test_select_and_compact_in_a_graph():
+    import torch
+    import head_latent_attention_split_b200 as mla
+    B, S, bs, budget = 3, 640, 64, 200
+    kv = torch.randn(B * 10 + B * 4, bs, 576, device="cuda").bfloat16()
+    perm = torch.randperm(B * 14, generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    bt, dt = perm[:B * 10].reshape(B, 10).contiguous(), perm[B * 10:].reshape(B, 4).contiguous()
+    mass, lens = torch.rand(B, S, device="cuda"), torch.tensor([640, 100, 333], dtype=torch.int32, device="cuda")
+    idx, cnt = torch.empty(B, budget, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+    out = torch.empty(B, 256, device="cuda")
+
+    def step():
+        mla.evict_select(mass, lens, budget, sinks=4, recent=50, indices=idx, counts=cnt)
+        mla.cache_compact(kv, bt, dt, idx, cnt, mass=mass, mass_out=out)
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    mass.copy_(torch.rand(B, S, generator=torch.Generator().manual_seed(2)))
+    lens.copy_(torch.tensor([200, 640, 201], dtype=torch.int32))
+    g.replay()
+    torch.cuda.synchronize()
+    assert mla.device_status() == 0
+    ref_i, ref_c = R.evict(mass.cpu().numpy(), lens.cpu().numpy(), budget, 4, 50)
+    np.testing.assert_array_equal(idx.cpu().numpy(), ref_i)
+    np.testing.assert_array_equal(cnt.cpu().numpy(), ref_c)
+    flat = kv.reshape(-1, 576)
+    for b in range(B):
+        t = torch.from_numpy(ref_i[b, :ref_c[b]].astype(np.int64)).cuda()
+        j = torch.arange(ref_c[b], device="cuda")
+        assert torch.equal(flat[dt[b, j // bs].long() * bs + j % bs], flat[bt[b, t // bs].long() * bs + t % bs])
+        assert torch.equal(out[b, :ref_c[b]], mass[b, t]) and bool((out[b, ref_c[b]:] == 0).all())

@@ -155,3 +155,53 @@ def test_graph_replay_and_other_stream():
     # the lse of the longer lengths stays a valid input
     check(dict(inp, seq_lens=np.array([690, 1, 1290], np.int32)), lse, mass_in * 2, mass, -7.0)
     assert mla.device_status() == 0
+
+
+@pytest.mark.parametrize("w", [BF16, MTP, FP8], ids=["bf16", "two-groups", "fp8"])
+def test_an_expired_wait_ends_cleanly(w):
+    import torch
+    import head_latent_attention_split_b200 as mla
+    w = w.with_(B=3, seq_lens=(900, 300, 1500))
+    inp, lse, mass_in = setup(w)
+    mass = torch.full(mass_in.shape, -7.0, device="cuda")
+    mla.set_wait_timeout_ns(200)
+    try:
+        st = run(inp, lse, mass_in.cuda(), mass)
+    finally:
+        mla.set_wait_timeout_ns(0)
+    assert st == 8 and mla.device_status() == 0
+    assert bool(mass.isnan().any())
+    mass.fill_(-7.0)
+    assert run(inp, lse, mass_in.cuda(), mass) == 0
+    check(inp, lse, mass_in, mass, -7.0)
+
+
+def test_a_large_batch_of_short_and_empty_sequences():
+    import torch
+    rng = np.random.default_rng(4)
+    lens = tuple(int(x) for x in rng.integers(0, 300, 200))
+    for w in (BF16.with_(B=200, H=4, seq_lens=lens), FP8.with_(B=200, H=4, seq_lens=lens), F32.with_(B=200, seq_lens=lens)):
+        inp, lse, mass_in = setup(w)
+        mass = torch.full(mass_in.shape, -7.0, device="cuda")
+        assert run(inp, lse, mass_in.cuda(), mass) == 0
+        check(inp, lse, mass_in, mass, -7.0)
+
+
+def test_front_end_refuses_tensors_that_do_not_fit():
+    import torch
+    import head_latent_attention_split_b200 as mla
+    w = BF16.with_(B=2, seq_lens=(70, 130), H=16)
+    t = W.to_torch(W.make_inputs(w))
+    good = dict(q_lat=t["q_lat"], q_rope=t["q_rope"], kv_cache=t["kv_cache"], block_table=t["block_table"],
+                seq_lens=t["seq_lens"], lse=torch.zeros(2, 1, 16, device="cuda"), softmax_scale=w.scale,
+                mass=torch.zeros(2, 130, device="cuda"))
+    mla.attention_mass(**good)
+    for bad in (dict(lse=torch.zeros(2, 16, device="cuda")), dict(mass=torch.zeros(3, 130, device="cuda")),
+                dict(mass=torch.zeros(130, 2, device="cuda").T), dict(mass_in=torch.zeros(2, 131, device="cuda")),
+                dict(mass=torch.zeros(2, 130, device="cuda").double()), dict(q_rope=None), dict(seq_lens=t["seq_lens"].long())):
+        with pytest.raises((TypeError, ValueError)):
+            mla.attention_mass(**{**good, **bad})
+    with pytest.raises(mla.MlaError):
+        mla.attention_mass(**{**good, "kernel": "tc_pair"})
+    torch.cuda.synchronize()
+    assert mla.device_status() == 0

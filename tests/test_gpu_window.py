@@ -213,3 +213,57 @@ def test_front_end_refuses_tensors_that_do_not_fit():
         call(out=torch.empty(args[0].shape, device="cuda"))
     torch.cuda.synchronize()
     assert mla.device_status() == 0
+
+
+@pytest.mark.parametrize("w,kernel", [(BF16, "tc_pair"), (BF16, "tcgen05"), (FP8, "tc_pair"), (FP8, "tcgen05")],
+                         ids=["bf16-pair", "bf16-tcgen05", "fp8-pair", "fp8-tcgen05"])
+def test_an_expired_wait_ends_cleanly(w, kernel):
+    import torch
+    import head_latent_attention_split_b200 as mla
+    w = w.with_(B=3, seq_lens=(900, 300, 1500))
+    inp = W.make_inputs(w)
+    ref = R.window(inp, 600, 4)
+    mla.set_wait_timeout_ns(200)
+    try:
+        out, lse, st = run(inp, 600, 4, kernel=kernel)
+    finally:
+        mla.set_wait_timeout_ns(0)
+    assert st == 8 and mla.device_status() == 0
+    nan = lse.isnan()
+    assert bool(nan.any()) and bool(out[nan].isnan().all())
+    out, lse, st = run(inp, 600, 4, kernel=kernel)
+    assert st == 0
+    close(out, lse, ref)
+
+
+def test_buffers_are_not_written_past_their_ends():
+    import torch
+    import head_latent_attention_split_b200 as mla
+    for w, win in ((MTP.with_(B=3, H=20, seq_lens=(700, 65, 1300)), 300), (FP8.with_(B=3, H=40, seq_lens=(700, 0, 1300)), 600),
+                   (F32.with_(B=3, seq_lens=(100, 0, 64)), 30)):
+        inp = W.make_inputs(w)
+        t = W.to_torch(inp)
+        p = mla.params_for(t["q_lat"], t["q_rope"], t["kv_cache"], t["block_table"], w.scale, w.causal)
+        need, n, guard = mla.workspace_size(p), t["q_lat"].numel(), 4096
+        ob = torch.full((n + 2 * guard,), 7.0, dtype=t["q_lat"].dtype, device="cuda")
+        lb = torch.full((n // w.r + 2 * guard,), 7.0, device="cuda")
+        wb = torch.full((need + 2 * guard,), 0xA5, dtype=torch.uint8, device="cuda")
+        out, lse = ob[guard:guard + n].view(t["q_lat"].shape), lb[guard:guard + n // w.r].view(t["q_lat"].shape[:3])
+        mla.window_decode(t["q_lat"], t["q_rope"], t["kv_cache"], t["block_table"], t["seq_lens"], w.scale, win, sinks=2,
+                          causal=w.causal, k_rope_cache=t["k_rope_cache"], kv_scale=t["kv_scale"], out=out, lse=lse,
+                          workspace=wb[guard:guard + need])
+        torch.cuda.synchronize()
+        assert mla.device_status() == 0
+        for buf, v in ((ob, 7.0), (lb, 7.0), (wb, 0xA5)):
+            assert bool((buf[:guard] == v).all()) and bool((buf[-guard:] == v).all())
+        close(out, lse, R.window(inp, win, 2))
+
+
+def test_a_large_batch_of_short_and_empty_sequences():
+    rng = np.random.default_rng(3)
+    lens = tuple(int(x) for x in rng.integers(0, 400, 300))
+    for w in (BF16.with_(B=300, H=4, seq_lens=lens), FP8.with_(B=300, H=4, seq_lens=lens), F32.with_(B=300, seq_lens=lens)):
+        inp = W.make_inputs(w)
+        out, lse, st = run(hide(inp, 90, 3), 90, 3)
+        assert st == 0
+        close(out, lse, R.window(inp, 90, 3))
