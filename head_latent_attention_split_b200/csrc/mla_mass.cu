@@ -124,9 +124,9 @@ constexpr int kMaxSlots = 12;
 constexpr int kQChunks = 9;                      // query: 9 x [N rows][128 bytes]
 constexpr int kGroupRows = 128;                  // query rows per group (at most)
 constexpr int kGroupRun = 4;                     // tiles per run when there are several groups
-// warps 0-7 sums (0-3 the even tiles, 4-7 the odd ones), 8 TMA, 9 MMA, 10-13 query split (e4m3)
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kSplitWarp = 10;
-constexpr int kTcThreads = 32 * 14;
+// warps 0-7 sums (0-3 the even tiles, 4-7 the odd ones) and, for an e4m3 cache, the query's split; 8 TMA, 9 MMA
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kTcThreads = 32 * 10;
 constexpr uint32_t kCtlBytes = 2048;             // leaves 5 ring slots at 128 rows
 constexpr uint32_t kSmemMax = 232448;
 
@@ -147,7 +147,6 @@ struct MassCtl {
   alignas(16) float a2[kGroupRows];    // e4m3: the row's power of two * scale * log2(e)
   uint8_t late[kGroupRows];  // causal: query tokens between the group's first row and this one
   uint32_t flags[kTileFlags];
-  uint8_t pow2[kGroupRows];  // e4m3: exponent field of the row's power of two (split warps -> sum warps)
 };
 static_assert(sizeof(MassCtl) <= kCtlBytes, "control block");
 
@@ -201,10 +200,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(smem_u32(&ctl.empty[i]), 1);
     }
     for (int i = 0; i < kQChunks; ++i) {
-      mbar_init(smem_u32(&ctl.q_full[i]), kFp8 && i == 0 ? 4 : 1);   // e4m3: one arrival per split warp
-      // e4m3: the split warps also wait for the sum warps to have read the item's powers of two, which
-      // keeps q_full[0] at most one phase ahead of them
-      mbar_init(smem_u32(&ctl.q_empty[i]), kFp8 && i == 0 ? 2 : 1);
+      mbar_init(smem_u32(&ctl.q_full[i]), kFp8 && i == 0 ? 8 : 1);   // e4m3: one arrival per sum warp
+      mbar_init(smem_u32(&ctl.q_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctl.acc_full[i]), 1);
@@ -261,7 +258,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
           for (int j = 0; j < kChunks; ++j) {
             const bool rope = j == kChunks - 1;
-            if (t == t0 && (!kFp8 || rope)) {   // the item's query chunk (e4m3: the split warps write the latent part)
+            if (t == t0 && (!kFp8 || rope)) {   // the item's query chunk (e4m3: the sum warps write the latent part)
               const int qj = rope ? kQChunks - 1 : j;
               if (!mbar_wait<false>(smem_u32(&ctl.q_empty[qj]), (item & 1) ^ 1, abort, timeout_ns)) return false;
               const uint32_t bar = smem_u32(&ctl.q_full[qj]);
@@ -352,10 +349,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int kk = 0; kk < 4; ++kk) mma_ss(dd, ad + 2 * kk, bd + 2 * kk, idesc16, (kFp8 ? kk : j | kk) ? 1u : 0u);
           }
           mma_commit(smem_u32(&ctl.empty[slot]));
-          if ((flags & kLast) && (!kFp8 || rope)) {   // the query's chunk is free (e4m3: all of it) for the next item
-            mma_commit(smem_u32(&ctl.q_empty[rope ? kQChunks - 1 : j]));
-            if (kFp8) mma_commit(smem_u32(&ctl.q_empty[0]));
-          }
+          // the query's chunk is free for the next item (e4m3: the latent part is when the sums are done)
+          if ((flags & kLast) && (!kFp8 || rope)) mma_commit(smem_u32(&ctl.q_empty[rope ? kQChunks - 1 : j]));
           if (rope) mma_commit(smem_u32(&ctl.acc_full[u & 1]));
         }
         if (++slot == slots) {
@@ -372,15 +367,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncwarp();
     mbar_wait<false>(smem_u32(&ctl.drain), 0, &dummy, drain_ns);
     if (!ok && lane == 0) set_status(a.status, MLA_ERR_TIMEOUT);
-  } else if (warp >= kSplitWarp) {
-    // ---------------------------------------------------------------- e4m3: the query in two terms
-    if constexpr (kFp8) {
-      uint32_t item = 0;
-      const bool ok = for_items([&](int b, int, int g, int, int) {
-        if (!__all_sync(0xffffffffu, mbar_wait<false>(smem_u32(&ctl.q_empty[0]), (item & 1) ^ 1, abort, timeout_ns)))
-          return false;
+  } else {
+    // ---------------------------------------------------------------- sums (thread = token)
+    // Two sets of four warps take the tiles of even and odd number, so that one set's TMEM loads and
+    // exponentials overlap the other's; a token is always one thread's.
+    const int tr = threadIdx.x & 127, set = threadIdx.x >> 7;   // tr: TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const float qnan = __uint_as_float(0x7FC00000u);
+    const unsigned long long scale2 = f2_pack(a.scale_log2, a.scale_log2);
+    uint32_t u = 0;
+    bool ok = true;
+    for_items([&](int b, int Lc, int g, int t0, int t1) {
+      const int s_first = g * kGroupRows / a.H;   // query token of the group's first row
+      // all sum warps are done with the previous item's rows
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (set == 0) {
+        const int row = g * kGroupRows + tr;
+        const bool valid = row < a.rows && tr < N;
+        ctl.nl2[tr] = valid ? -__ldg(m.lse + (size_t)b * a.rows + row) * kLog2e : -INFINITY;
+        ctl.late[tr] = valid ? (uint8_t)(row / a.H - s_first) : 0;
+      }
+      if constexpr (kFp8) {
+        // the group's query in two terms. Its last readers were the previous item's MMAs, and their last
+        // sums are done.
         constexpr int kU = 4;   // rows in flight per warp
-        for (int r0 = kU * (warp - kSplitWarp); r0 < N; r0 += 4 * kU) {
+        for (int r0 = kU * warp; r0 < N; r0 += 8 * kU) {
           uint4 v[kU][2];
 #pragma unroll
           for (int i = 0; i < kU; ++i) {
@@ -400,43 +411,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint8_t* dst = gQ + (lane >> 3) * q_chunk + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
             *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4*>(dst + 4 * q_chunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            if (lane == 0) ctl.pow2[r] = (uint8_t)up;
+            if (lane == 0) ctl.a2[r] = __uint_as_float(up << 23) * a.scale_log2;
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl.q_full[0]));
-        ++item;
-        return true;
-      });
-      if (!ok) set_status(a.status, MLA_ERR_TIMEOUT);
-    }
-  } else {
-    // ---------------------------------------------------------------- sums (thread = token)
-    // Two sets of four warps take the tiles of even and odd number, so that one set's TMEM loads and
-    // exponentials overlap the other's; a token is always one thread's.
-    const int tr = threadIdx.x & 127, set = threadIdx.x >> 7;   // tr: TMEM lane
-    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const float qnan = __uint_as_float(0x7FC00000u);
-    const unsigned long long scale2 = f2_pack(a.scale_log2, a.scale_log2);
-    uint32_t item = 0, u = 0;
-    bool ok = true;
-    for_items([&](int b, int Lc, int g, int t0, int t1) {
-      const int s_first = g * kGroupRows / a.H;   // query token of the group's first row
-      // the group's rows (all sum warps are done with the previous item's)
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (kFp8 && ok)
-        ok = __all_sync(0xffffffffu, mbar_wait<false>(smem_u32(&ctl.q_full[0]), item & 1, abort, timeout_ns));
-      if (set == 0) {
-        const int row = g * kGroupRows + tr;
-        const bool valid = row < a.rows && tr < N;
-        ctl.nl2[tr] = valid ? -__ldg(m.lse + (size_t)b * a.rows + row) * kLog2e : -INFINITY;
-        ctl.late[tr] = valid ? (uint8_t)(row / a.H - s_first) : 0;
-        if constexpr (kFp8)
-          ctl.a2[tr] = tr < N ? __uint_as_float((uint32_t)ctl.pow2[tr] << 23) * a.scale_log2 : 0.f;
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (kFp8 && threadIdx.x == 0) mbar_arrive(smem_u32(&ctl.q_empty[0]));
       const int least = Lc - a.Sq + 1 + s_first;   // causal: every row of the group sees the tokens before this one
       for (int t = t0; t < t1; ++t, ++u) {
         if ((t & 1) != set) continue;
@@ -520,7 +502,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         f2_unpack(sum[1], p2, p3);
         if (mine) *out = good ? before + ((p0 + p1) + (p2 + p3)) : qnan;
       }
-      ++item;
       return true;
     });
     if (!ok) set_status(a.status, MLA_ERR_TIMEOUT);
