@@ -225,7 +225,7 @@ mla_status_t decode_impl(const mla_decode_params_t* p, const void* q_lat, const 
   mla::DecodeArgs a = make_args(p, W);
   a.window = window < a.len_cap ? window : a.len_cap;   // 0: every token before the row
   a.sinks = sinks < a.len_cap ? sinks : a.len_cap;
-  a.whole = kernel != MLA_KERNEL_SIMT;
+  a.aligned = kernel != MLA_KERNEL_SIMT;
   a.q_lat = q_lat;
   a.q_rope = q_rope;
   a.cache = kv_cache;

@@ -98,13 +98,13 @@ struct DenseTiles {
   __device__ __forceinline__ int count(int Lc) const { return tiles_of(Lc, bs); }
   __device__ __forceinline__ int block(int i, int) const { return i; }
   __device__ __forceinline__ int gap(int) const { return 0; }
-  __device__ __forceinline__ int whole_run(long long, int, int, int, int) const { return 0; }
+  __device__ __forceinline__ int cut(long long, int, int, int, int) const { return 0; }
 };
 
 struct WindowTiles {
-  int bs, Sq, causal, window, sinks, whole;
+  int bs, Sq, causal, window, sinks, aligned;
   __device__ __forceinline__ WindowTiles(const DecodeArgs& a)
-      : bs(a.bs), Sq(a.Sq), causal(a.causal), window(a.window), sinks(a.sinks), whole(a.whole) {}
+      : bs(a.bs), Sq(a.Sq), causal(a.causal), window(a.window), sinks(a.sinks), aligned(a.aligned) {}
   // first token of the earliest window among the sequence's query rows
   __device__ __forceinline__ int lo(int Lc) const {
     const int first = causal ? max(Lc - Sq + 1, 0) : Lc;
@@ -114,16 +114,28 @@ struct WindowTiles {
   __device__ __forceinline__ int gap(int Lc) const { return max(lo(Lc) / bs - sink_tiles(Lc), 0); }
   __device__ __forceinline__ int count(int Lc) const { return tiles_of(Lc, bs) - gap(Lc); }
   __device__ __forceinline__ int block(int i, int Lc) const { return i < sink_tiles(Lc) ? i : i + gap(Lc); }
-  // Sequences per worker when each worker takes whole sequences, 0 when the tile list is cut evenly.
-  // A window's tile lists are short and nearly all alike, so whole sequences are often almost as even, and
-  // they cost no partial outputs, nothing to merge and fewer segments per worker. Worth it while the
-  // longest share exceeds the even one by no more tiles than that saves, as measured on 74 workers, 128
-  // rows, bf16 (even cut, whole): 64 sequences of 65 tiles 129, 111 us; 40 of 33 77, 70; 8 of 33 54, 60;
-  // two per worker: 80 of 8 67, 57; 80 of 17 80, 81; a tile or less per worker: 8 of 8 40, 33.
+  // How the tile list is cut among the workers: k > 0 sequences per worker, -k > 0 workers per sequence, or
+  // 0: evenly, wherever that falls (see WorkerPlan). A window's tile lists are short and nearly all alike, and
+  // a worker's second segment costs as much as 10 to 20 tiles (its query, the drained pipeline, the
+  // epilogue), so cuts at the sequences' ends are worth a longer share; whole sequences have no partial
+  // outputs and nothing to merge besides. Measured on 74 workers, 128 rows, bf16, us (even cut, whole,
+  // parts), n sequences x tiles:
+  //   a few sequences, parts of at least 4 tiles: 1 x 33: 39, 55, 33; 9 x 33: 44, 56, 36; 3 x 9: 31, 31, 31
+  //   (e4m3 39, 46, 39);
+  //   two to four workers per sequence: 32 x 9: 47, 33, 39 (e4m3 65, 47, 49); 16 x 17: 45, 39, 36;
+  //   32 x 17: 54, 41, 43 (e4m3 74, 61, 56); 32 x 65: 84, 93, 74;
+  //   a longest share 12 tiles above the even one: 15 x 257: 109, -, 109;
+  //   one worker or less per sequence: 64 x 65: 129, 111; 40 x 33: 77, 70; 80 x 8: 67, 57; 80 x 17: 80, 81.
   // Where nothing is hidden the cut stays the dense one, and with it the result.
-  __device__ __forceinline__ int whole_run(long long T, int most, int hidden, int B, int W) const {
-    const int k = (B + W - 1) / W, more = T <= 2 * W ? 12 : k == 1 ? 22 : 16;
-    return whole && hidden > 0 && (long long)k * most <= T / W + more ? k : 0;
+  __device__ __forceinline__ int cut(long long T, int most, int hidden, int B, int W) const {
+    if (!aligned || hidden == 0) return 0;
+    const int k = (B + W - 1) / W, p = min(min(W / B, (most + 3) / 4), 32);
+    if (p > 1) {
+      const int share = (most + p - 1) / p;
+      if (most - share > 5) return share <= T / W + 12 ? -p : 0;
+    }
+    const int more = T <= 2 * W ? 12 : k == 1 ? 22 : 16;
+    return (long long)k * most <= T / W + more ? k : 0;
   }
 };
 
@@ -151,14 +163,16 @@ struct WindowCols {
 };
 
 //
-// When tiles.whole_run() says so (k > 0), worker w owns sequences [k w, k (w + 1)) instead, whole.
+// When tiles.cut() says so, workers are aligned to sequences instead: worker w owns sequences
+// [k w, k (w + 1)) whole (k > 0), or part w % p of sequence w / p (p = -k > 0 workers each, of which the
+// first min(p, tiles) have a part).
 
 struct WorkerPlan {
   long long T;      // total tiles
   int W;            // active workers, min(W, T)
-  int whole;        // sequences per worker, or 0: the even cut
-  long long start;  // first tile of this worker
-  long long end;    // one past its last tile
+  int cut;          // sequences per worker, -(workers per sequence), or 0: the even cut
+  long long start;  // first tile of this worker (workers per sequence: its part)
+  long long end;    // one past its last tile (aligned to sequences: one past its last sequence)
   long long P0;     // flat index of sequence b0's first tile
   int b0;           // first sequence with a tile in [start, end)
 };
@@ -183,12 +197,14 @@ __device__ __forceinline__ WorkerPlan warp_plan(const int32_t* __restrict__ seq_
   p.T = T;
   p.W = (T > 0 && T < W) ? (int)T : W;
   hidden = __reduce_max_sync(0xffffffffu, hidden);
-  p.whole = tiles.whole_run(T, most, hidden, B, W);
-  if (p.whole) {
+  p.cut = tiles.cut(T, most, hidden, B, W);
+  if (p.cut) {
+    const int parts = max(-p.cut, 1), k = max(p.cut, 1);   // one of them is 1
     p.W = W;
-    p.b0 = (int)min((long long)w * p.whole, (long long)B);
-    p.start = p.P0 = 0;
-    p.end = min((long long)(w + 1) * p.whole, (long long)B);   // one past the worker's last sequence
+    p.b0 = (int)min((long long)(w / parts) * k, (long long)B);
+    p.start = w % parts;
+    p.P0 = 0;
+    p.end = min((long long)(w / parts + 1) * k, (long long)B);
     return p;
   }
   p.start = (T > 0 && w < p.W) ? (long long)w * T / p.W : T;
@@ -250,16 +266,19 @@ struct SegmentIterT {
       : seq_lens(sl), tiles(t), B(B_), cap(cap_), W(plan.W), w(w_), status(st), p(plan), b(plan.b0), P(plan.P0) {}
 
   __device__ bool next(Segment& sg) {
-    while (p.whole && b < (int)p.end) {
+    while (p.cut && b < (int)p.end) {
       sg.Lc = clamp_len(__ldg(seq_lens + b), cap, status);
       sg.b = b++;
-      sg.tile_begin = sg.split = 0;
-      sg.tile_end = tiles.count(sg.Lc);
-      sg.first_worker = w;
-      sg.splits = 1;
-      if (sg.tile_end > 0) return true;
+      const int n = tiles.count(sg.Lc);
+      sg.split = (int)p.start;
+      sg.first_worker = w - sg.split;
+      sg.splits = min(max(-p.cut, 1), n);
+      if (sg.split >= sg.splits) continue;   // (no tile at all among them)
+      sg.tile_begin = (int)((long long)n * sg.split / sg.splits);
+      sg.tile_end = (int)((long long)n * (sg.split + 1) / sg.splits);
+      return true;
     }
-    if (p.whole) return false;
+    if (p.cut) return false;
     while (b < B && P < p.end) {
       const int Lc = clamp_len(__ldg(seq_lens + b), cap, status);
       const int n = tiles.count(Lc);

@@ -34,7 +34,7 @@ struct DecodeArgs {
   const int32_t* sel_idx;      // sparse decode only: [B, top_k] selected positions, else null
   int top_k;                   // sparse decode only: row stride of sel_idx
   int window, sinks;           // window decode only (window >= 1): tokens a row sees at the end and at the start
-  int whole;                   // ... workers may take whole sequences (the tensor-core kernels' costs)
+  int aligned;                 // ... workers may be aligned to sequences (the tensor-core kernels' costs)
   void* out;                   // [B, Sq, H, r] out_dtype
   float* lse;                  // [B, Sq, H]
   // workspace

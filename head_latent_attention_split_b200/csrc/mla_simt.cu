@@ -244,8 +244,11 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
   const float qnan = __uint_as_float(0x7FC00000u);
   const long long n = raw < 0 || raw > cap ? 0 : tiles.count(raw);
   int first = 0, splits = 0;
-  if (n > 0 && tiles.whole_run(total, most, hidden, a.B, a.W)) {
-    splits = 1;
+  const int cut = tiles.cut(total, most, hidden, a.B, a.W);
+  if (n > 0 && cut) {
+    const int parts = max(-cut, 1);
+    first = b * parts;
+    splits = (int)min((long long)parts, n);
   } else if (n > 0) {
     const int Wa = (total < a.W) ? (int)total : a.W;
     first = worker_of_tile(before, total, Wa);
@@ -326,19 +329,28 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
         }
         i0 = 2;
       }
-#pragma unroll 2
-      for (int i = i0; i < splits; ++i) {
-        const size_t prow = (slot0 + i) * a.rows + row;
-        const float wgt = i < 32 ? __shfl_sync(0xffffffffu, wl, i) : expf(a.lse_part[prow] - lse_v);
-        if (wgt == 0.f) continue;
-        const float* src = a.o_part + prow * a.r;
-        float4 v[4];
+      constexpr int kG = 4;   // splits whose pieces are on their way together; added in order
+#pragma unroll 1
+      for (int i = i0; i < splits; i += kG) {
+        float4 v[kG][4];
+        float late[kG];       // log-sum-exps behind the 32 that the lanes hold
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int k = k0 + 4 * lane + 128 * u;
-          v[u] = k < a.r ? *reinterpret_cast<const float4*>(src + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < kG; ++j) {
+          const size_t prow = (slot0 + i + j) * a.rows + row;
+          const float* src = a.o_part + prow * a.r;
+          late[j] = i + j >= 32 && i + j < splits ? a.lse_part[prow] : 0.f;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int k = k0 + 4 * lane + 128 * u;
+            v[j][u] = i + j < splits && k < a.r ? *reinterpret_cast<const float4*>(src + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
         }
-        add(wgt, v);
+#pragma unroll
+        for (int j = 0; j < kG; ++j) {
+          const float held = __shfl_sync(0xffffffffu, wl, (i + j) & 31);
+          const float wgt = i + j >= splits ? 0.f : i + j < 32 ? held : expf(late[j] - lse_v);
+          if (wgt != 0.f) add(wgt, v[j]);
+        }
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
