@@ -6,6 +6,7 @@
 // memory in chunks of tokens decoded to fp32 (bf16 / e4m3 * scale / f32); every warp
 // scores the chunk against its row's absorbed query with an fp32 online softmax in
 // base 2 (score * scale * log2 e) and accumulates the latent rows as values.
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 
@@ -188,76 +189,13 @@ __global__ void __launch_bounds__(kThreads) simt_decode_kernel(const DecodeArgs 
   }
 }
 
-// One warp per (b, row): merge the partials of split sequences, fill empty ones. The split of
-// each sequence is recomputed here from seq_lens with the plan's formula (nothing read from the
-// workspace is trusted for indexing). Rows of a sequence with a seq_len out of range, and rows
-// whose partials carry a NaN log-sum-exp (a decode wait timed out, or a bad block id), are
-// written as NaN.
-// A chain of latencies bounds it (a few MB of partials, in L2): lengths, log-sum-exps, partials. So the
-// window decode launches it as a dependent of the decode kernel, with the lengths read and the
-// split found while that kernel still runs, and the partials of the first splits are requested before
-// their weights are known.
-template <bool kWindow>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
-  __shared__ long long s_sum[kWarps][2];
-  __shared__ int s_most[kWarps][2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.x;
-  const int cap = a.len_cap;
-  const auto tiles = TilesOf<kWindow>::make(a);
-  // tiles before sequence b and in total, as the decode kernels' plan counts them
-  long long before = 0, total = 0;
-  int most = 0, hidden = 0;
-  for (int i = threadIdx.x; i < a.B; i += kThreads) {
-    const int L = __ldg(a.seq_lens + i), Lc = L < 0 ? 0 : (L > cap ? cap : L);
-    const int n = tiles.count(Lc);
-    total += n;
-    most = max(most, n);
-    hidden = max(hidden, tiles.gap(Lc));
-    if (i < b) before += n;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-  }
-  most = __reduce_max_sync(0xffffffffu, most);
-  hidden = __reduce_max_sync(0xffffffffu, hidden);
-  if (lane == 0) {
-    s_sum[warp][0] = before;
-    s_sum[warp][1] = total;
-    s_most[warp][0] = most;
-    s_most[warp][1] = hidden;
-  }
-  __syncthreads();
-  before = total = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    before += s_sum[i][0];
-    total += s_sum[i][1];
-    most = max(most, s_most[i][0]);
-    hidden = max(hidden, s_most[i][1]);
-  }
-  const int row = blockIdx.y * kWarps + warp;
+// One row's output and log-sum-exp from its `splits` partials (not 1), by one warp; none: zeros, or NaN behind a
+// length that is out of range.
+__device__ __forceinline__ void combine_row(const DecodeArgs& a, int b, int row, int first, int splits, bool bad) {
+  const int lane = threadIdx.x & 31;
   const size_t orow = (size_t)b * a.rows + row;
-  const int raw = __ldg(a.seq_lens + b);
   const float qnan = __uint_as_float(0x7FC00000u);
-  const long long n = raw < 0 || raw > cap ? 0 : tiles.count(raw);
-  int first = 0, splits = 0;
-  const int cut = tiles.cut(total, most, hidden, a.B, a.W);
-  if (n > 0 && cut) {
-    const int parts = max(-cut, 1);
-    first = b * parts;
-    splits = (int)min((long long)parts, n);
-  } else if (n > 0) {
-    const int Wa = (total < a.W) ? (int)total : a.W;
-    first = worker_of_tile(before, total, Wa);
-    splits = worker_of_tile(before + n - 1, total, Wa) - first + 1;
-  }
-  if constexpr (kWindow) ptx::wait_for_grid_before();   // every thread, so that this grid ends after the decode's
-  if (row >= a.rows || splits == 1) return;             // (one split: the decode wrote the row directly)
   if (splits == 0) {
-    const bool bad = raw < 0 || raw > cap;
     for (int k = lane; k < a.r; k += 32) store_out(a.out, a.out_dtype, orow * a.r + k, bad ? qnan : 0.f);
     if (lane == 0) a.lse[orow] = bad ? qnan : -INFINITY;
     return;
@@ -329,7 +267,9 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
         }
         i0 = 2;
       }
-      constexpr int kG = 4;   // splits whose pieces are on their way together; added in order
+      // splits whose pieces are on their way together, added in order (1 sequence of 65 tiles in 17 parts: 36.0 us
+      // with 2, 37.0 with 3, 38.2 with 4, whose registers spill)
+      constexpr int kG = 2;
 #pragma unroll 1
       for (int i = i0; i < splits; i += kG) {
         float4 v[kG][4];
@@ -397,6 +337,76 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeArgs a) {
   if (lane == 0) a.lse[orow] = lse_v;
 }
 
+// One warp per (b, row): merge the partials of split sequences, fill empty ones. The split of
+// each sequence is recomputed here from seq_lens with the plan's formula (nothing read from the
+// workspace is trusted for indexing). Rows of a sequence with a seq_len out of range, and rows
+// whose partials carry a NaN log-sum-exp (a decode wait timed out, or a bad block id), are
+// written as NaN.
+// A chain of latencies bounds it (a few MB of partials, in L2): lengths, log-sum-exps, partials. So the
+// window decode launches it as a dependent of the decode kernel, with the lengths read and the
+// split found while that kernel still runs, and the partials of the first splits are requested before
+// their weights are known.
+template <bool kWindow>
+__global__ void __launch_bounds__(kThreads, 2) combine_kernel(const DecodeArgs a) {
+  __shared__ long long s_sum[kWarps][2];
+  __shared__ int s_most[kWarps][2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.x;
+  const int cap = a.len_cap;
+  const auto tiles = TilesOf<kWindow>::make(a);
+  // tiles before sequence b and in total, as the decode kernels' plan counts them
+  long long before = 0, total = 0;
+  int most = 0, hidden = 0;
+  for (int i = threadIdx.x; i < a.B; i += kThreads) {
+    const int L = __ldg(a.seq_lens + i), Lc = L < 0 ? 0 : (L > cap ? cap : L);
+    const int n = tiles.count(Lc);
+    total += n;
+    most = max(most, n);
+    hidden = max(hidden, tiles.gap(Lc));
+    if (i < b) before += n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  hidden = __reduce_max_sync(0xffffffffu, hidden);
+  if (lane == 0) {
+    s_sum[warp][0] = before;
+    s_sum[warp][1] = total;
+    s_most[warp][0] = most;
+    s_most[warp][1] = hidden;
+  }
+  __syncthreads();
+  before = total = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    before += s_sum[i][0];
+    total += s_sum[i][1];
+    most = max(most, s_most[i][0]);
+    hidden = max(hidden, s_most[i][1]);
+  }
+  const int raw = __ldg(a.seq_lens + b);
+  const float qnan = __uint_as_float(0x7FC00000u);
+  const long long n = raw < 0 || raw > cap ? 0 : tiles.count(raw);
+  int first = 0, splits = 0;
+  const int cut = tiles.cut(total, most, hidden, a.B, a.W);
+  if (n > 0 && cut) {
+    const int parts = max(-cut, 1);
+    first = b * parts;
+    splits = (int)min((long long)parts, n);
+  } else if (n > 0) {
+    const int Wa = (total < a.W) ? (int)total : a.W;
+    first = worker_of_tile(before, total, Wa);
+    splits = worker_of_tile(before + n - 1, total, Wa) - first + 1;
+  }
+  if constexpr (kWindow) ptx::wait_for_grid_before();   // every thread, so that this grid ends after the decode's
+  if (splits == 1) return;                              // (the decode wrote the rows directly)
+  for (int row = blockIdx.y * kWarps + warp; row < a.rows; row += gridDim.y * kWarps)
+    combine_row(a, b, row, first, splits, raw < 0 || raw > cap);
+}
+
 __global__ void __launch_bounds__(32) plan_probe_kernel(const DecodeArgs a, int32_t* token_slot,
                                                          int32_t* token_worker) {
   const int w = blockIdx.x, lane = threadIdx.x;
@@ -437,7 +447,11 @@ cudaError_t launch_simt_decode(const DecodeArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t s) {
-  dim3 grid(a.B, (a.rows + kWarps - 1) / kWarps);
+  // Blocks for two per SM: a block finds its sequence's splits once and walks its rows. (With one block per eight
+  // rows, the 3072 blocks of 96 sequences x 256 rows with nothing to merge took 49 us by themselves.)
+  constexpr int kSms = 148;
+  const int groups = (a.rows + kWarps - 1) / kWarps;
+  dim3 grid(a.B, std::max(1, std::min(groups, 2 * kSms / std::max(a.B, 1))));
   if (a.window > 0) {
     // a dependent of the decode kernel before it: its blocks may start while that kernel's last CTAs run
     cudaLaunchConfig_t cfg{};
