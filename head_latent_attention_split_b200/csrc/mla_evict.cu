@@ -28,8 +28,7 @@ using namespace ptx;
 
 // ------------------------------------------------------------------------------- select
 constexpr int kSelThreads = 1024;
-constexpr int kSelPer = 16;                            // consecutive keys per thread
-constexpr int kSelSpan = kSelThreads * kSelPer;        // positions per CTA and round
+constexpr int kSelPer = 16;                            // consecutive keys per thread, at most
 constexpr int kSelMaxCluster = 8;
 
 struct SelectArgs {
@@ -61,37 +60,37 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 
-// exclusive prefix sum over the block's 1024 threads; *total = the sum
-__device__ __forceinline__ uint64_t scan_excl(uint64_t v, uint64_t* wsum, uint64_t* total) {
+// Exclusive prefix sum over the block's 1024 threads; *total = the sum. One barrier: every warp sums up
+// the 32 warps' totals for itself. wsum is not written again before the block's next barrier but one.
+template <class T>
+__device__ __forceinline__ T scan_excl(T v, T* wsum, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t x = v;
+  T x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) wsum[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    uint64_t t = wsum[lane];
+  T t = wsum[lane];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t y = __shfl_up_sync(0xffffffffu, t, o);
-      if (lane >= o) t += y;
-    }
-    wsum[lane] = t;
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, t, o);
+    if (lane >= o) t += y;
   }
-  __syncthreads();
-  const uint64_t ex = x - v + (warp ? wsum[warp - 1] : 0ull);
-  *total = wsum[31];
-  __syncthreads();
-  return ex;
+  *total = __shfl_sync(0xffffffffu, t, 31);
+  const T before = __shfl_sync(0xffffffffu, t, (warp - 1) & 31);
+  return x - v + (warp ? before : (T)0);
 }
 
+// kPer: consecutive keys per thread
+template <int kPer>
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const SelectArgs a) {
   __shared__ uint32_t hist[3][2048];
-  __shared__ uint64_t wsum[32];
-  __shared__ uint32_t pick[2];
+  __shared__ uint64_t wsum[2][32];
+  __shared__ uint32_t hsum[3][32];
+  __shared__ uint32_t pick[3][3];
   __shared__ uint32_t slice[2];   // this CTA's counts of keys above T and equal to T
   const int tid = threadIdx.x;
   const uint32_t C = cluster_size(), rank = cluster_ctarank();
@@ -116,18 +115,19 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
 
   const float* row = a.mass + (size_t)b * a.S;
   const bool vec = ((uintptr_t)row & 15) == 0;
-  // this CTA's positions: rounds of 16384 * C consecutive ones, 16384 per CTA
-  const int lo = (int)rank * kSelSpan + tid * kSelPer;
-  const int round = kSelSpan * (int)C;
+  // this CTA's positions: rounds of kSpan * C consecutive ones, kSpan per CTA
+  constexpr int kSpan = kSelThreads * kPer;
+  const int lo = (int)rank * kSpan + tid * kPer;
+  const int round = kSpan * (int)C;
   const bool once = s1 <= round;
-  uint32_t key[kSelPer];
+  uint32_t key[kPer];
   uint32_t in = 0;   // bit m: position p0 + m is a candidate
   auto load = [&](int p0) {
     in = 0;
 #pragma unroll
-    for (int m = 0; m < kSelPer; ++m) in |= (p0 + m >= s0 && p0 + m < s1) ? 1u << m : 0u;
+    for (int m = 0; m < kPer; ++m) in |= (p0 + m >= s0 && p0 + m < s1) ? 1u << m : 0u;
 #pragma unroll
-    for (int m = 0; m < kSelPer; m += 4) {
+    for (int m = 0; m < kPer; m += 4) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (vec && p0 + m + 4 <= a.S) {
         if ((in >> m) & 15u) v = __ldg(reinterpret_cast<const float4*>(row + p0 + m));
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
     uint32_t* h = hist[pass];
     for_rounds([&](int) {
 #pragma unroll
-      for (int m = 0; m < kSelPer; ++m)
+      for (int m = 0; m < kPer; ++m)
         if (((in >> m) & 1u) && (key[m] & pmask) == prefix) atomicAdd(&h[(key[m] >> shift) & dmask], 1u);
     });
     if (C > 1) cluster_sync(); else __syncthreads();
@@ -190,37 +190,41 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
         }
       }
     }
-    uint64_t tot;
-    const uint32_t above = (uint32_t)scan_excl((uint64_t)(c_hi + c_lo), wsum, &tot);
+    uint32_t tot;
+    const uint32_t above = scan_excl(c_hi + c_lo, hsum[pass], &tot);
+    uint32_t* found = pick[pass];   // digit, entries above it, entries of it
     if (above < rem && rem <= above + c_hi) {
-      pick[0] = (uint32_t)d_hi;
-      pick[1] = above;
+      found[0] = (uint32_t)d_hi;
+      found[1] = above;
+      found[2] = c_hi;
     } else if (above + c_hi < rem && rem <= above + c_hi + c_lo) {
-      pick[0] = (uint32_t)d_lo;
-      pick[1] = above + c_hi;
+      found[0] = (uint32_t)d_lo;
+      found[1] = above + c_hi;
+      found[2] = c_lo;
     }
     __syncthreads();
-    rem -= pick[1];
-    prefix |= pick[0] << shift;
+    rem -= found[1];
+    prefix |= found[0] << shift;
     pmask |= dmask << shift;
-    __syncthreads();   // pick is read before the next pass writes it
+    if (rem == found[2]) break;   // all of them stay: no lower digit decides anything
   }
   const uint32_t T = prefix;
 
   // Positions above T, and the first `rem` equal to T, in order. A round's CTAs follow one another:
   // each CTA's counts go to the higher ranks, the round's sum to the next round.
-  uint32_t run_gt = 0, run_tie = 0;   // kept before this round
+  uint32_t run_gt = 0, run_tie = 0, turn = 0;   // kept before this round, its number
   for_rounds([&](int p0) {
     uint32_t gt = 0, tie = 0;
 #pragma unroll
-    for (int m = 0; m < kSelPer; ++m) {
+    for (int m = 0; m < kPer; ++m) {
       if ((in >> m) & 1u) {
         gt += key[m] > T ? 1u : 0u;
         tie += key[m] == T ? 1u : 0u;
       }
     }
     uint64_t tot;
-    const uint64_t ex = scan_excl(((uint64_t)gt << 32) | tie, wsum, &tot);
+    const uint64_t ex = scan_excl(((uint64_t)gt << 32) | tie, wsum[turn & 1], &tot);
+    ++turn;
     uint32_t g_before = run_gt + (uint32_t)(ex >> 32), t_before = run_tie + (uint32_t)ex;
     if (C == 1) {
       run_gt += (uint32_t)(tot >> 32);
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
       cluster_sync();   // the counts are read before the next round, or before a CTA leaves
     }
 #pragma unroll
-    for (int m = 0; m < kSelPer; ++m) {
+    for (int m = 0; m < kPer; ++m) {
       if (!((in >> m) & 1u)) continue;
       if (key[m] > T) {
         out[s0 + g_before + min(t_before, rem)] = p0 + m;
@@ -423,7 +427,7 @@ mla_status_t mla_evict_select(const mla_evict_params_t* p, const float* mass, co
   if (!status) return MLA_ERR_CUDA;
   const SelectArgs a{p->batch, p->max_seq_len, p->budget, p->sinks, p->recent, mass, seq_lens, indices, counts, status};
   int C = 1;
-  while (C < kSelMaxCluster && C * kSelSpan < p->max_seq_len) C *= 2;
+  while (C < kSelMaxCluster && C * kSelThreads * kSelPer < p->max_seq_len) C *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(p->batch * C));
   cfg.blockDim = dim3(kSelThreads);
@@ -434,7 +438,10 @@ mla_status_t mla_evict_select(const mla_evict_params_t* p, const float* mass, co
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel, a) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  auto kernel = p->max_seq_len <= kSelThreads * 4   ? evict_select_kernel<4>
+                : p->max_seq_len <= kSelThreads * 8 ? evict_select_kernel<8>
+                                                    : evict_select_kernel<kSelPer>;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 mla_status_t mla_cache_compact(const mla_compact_params_t* p, void* kv_cache, void* k_rope_cache, float* kv_scale,
