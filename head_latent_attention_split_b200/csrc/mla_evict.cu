@@ -2,19 +2,20 @@
 // (mla_evict_select) and their copy into other blocks (mla_cache_compact). See include/mla_decode.h.
 //
 // Select: of the candidates [sinks, L - recent) of a sequence keep the k = budget - sinks - recent
-// largest, ties to the lower position. A three-pass radix select (11, 11, 10 bits of an
-// order-preserving key) finds the k-th largest key T and how many entries equal to T stay; one
-// prefix sum over (above T, equal to T) counts then places every kept position. A cluster of
-// C CTAs shares a row, C * 16384 >= its length where that goes (C <= 8): a thread holds 16
-// consecutive keys in registers, so a row is read from memory once. Each pass has its own
-// histogram, which every CTA sums over the cluster for itself: one cluster barrier per pass.
+// largest, ties to the lower position. A radix select in up to three passes (11, 11, 10 bits of an
+// order-preserving key; none below a digit whose entries all stay) finds the k-th largest key T and how
+// many entries equal to T stay; one prefix sum over (above T, equal to T) counts then places every kept
+// position. A thread holds 4, 8 or 16 consecutive keys in registers, so a row is read from memory
+// once, and a cluster of C CTAs shares a row of more than 16384 (C <= 8, rounds beyond). Each pass has
+// its own histogram, which every CTA sums over the cluster for itself: one cluster barrier per pass.
 // A row of a few KB to half a MB is far from any bandwidth: the barriers and the histogram's
-// shared-memory atomics bound it.
+// shared-memory atomics bound it. 64 rows of up to 8192 take 11.5 us, one row of 1100 9 us (15.5 us each
+// with 16 keys per thread, three passes and six barriers in each).
 //
 // Compact: a copy, bound by memory: every kept row read and written once. A warp takes 8 entries of
 // one sequence; 8 lanes look their slots up and each moves its row by bulk copies through shared
 // memory, so the bytes in flight cost no registers (six CTAs of 37 KB per SM for a bf16 row of
-// 1152 bytes).
+// 1152 bytes). 64 sequences of up to 2048 kept rows (126 MB read, as much written): 40 us.
 #include <algorithm>
 #include <mutex>
 

@@ -47,6 +47,15 @@
 //     what P holds, and its reference sits 2^4 below it: P s_t stays in [0, 2^8], and e4m3's smallest
 //     step (2^-9, of which both terms may lose half) costs at most 2^-13 of the largest term.
 //   Half the bytes per tile: twice the ring slots.
+//   Bound by the softmax warps, 3.4 us per tile pair at 128 rows (bf16 2.3): scores and scales 1.05,
+//   exponentials and the two terms 1.15, the message 0.55, the rest waiting; a segment's start costs
+//   another 11 us, most of it the query's split.
+//
+// kWindow: the tile list holds only the blocks that some row sees (WindowTiles), the softmax masks what a
+// row does not see of them, and the cut among the workers is WindowTiles::cut's. 128 heads, bf16: 64
+// sequences x 65 tiles in 100 us (3.1 TB/s of cache, 42 % of the tensor pipe's time); 96 sequences x 256 causal
+// rows, windows of 1500: 132 us; e4m3, 32 x 34 tiles: 72 us. Bound by the coupled latencies of the tile loop
+// (2.3 us per pair, of which the 36 score MMAs 1.4) and by a segment's 14 us around it.
 #include <cuda.h>
 
 #include <cmath>
@@ -491,8 +500,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = wait_warp(smem_u32(&ctl.q_empty), (seg & 1) ^ 1);
         if (ok) {
           // in blocks of 128 bytes per row: eight lanes read a row's block side by side (instruction i:
-          // row 8 (lane / 8) + i, piece lane % 8), then the pieces move to the row's own lane. Read one
-          // row per lane, this took 6-8 us of LSU requests instead of about 2.
+          // row 8 (lane / 8) + i, piece lane % 8), then the pieces move to the row's own lane. Read one row per
+          // lane (32 requests per load), a worker's first query took 8.5 us, like this 6.3.
           const int row0 = rg * kRows + 32 * quarter + (lane & ~7);   // query row of this lane group's first row
           const uint16_t* ql = (const uint16_t*)a.q_lat + ((size_t)sg.b * a.rows + row0) * kR + 256 * half + 8 * (lane & 7);
           const uint16_t* qr = (const uint16_t*)a.q_rope + ((size_t)sg.b * a.rows + row0) * kDR + 8 * (lane & 7);
@@ -1086,7 +1095,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool direct = sg.splits == 1;
       if (ok) tc_fence_after();
       // Eight lanes write 128 bytes of a row side by side (transpose_pieces): the row of instruction i is
-      // the group's i-th. One row per lane took 11 us for 128 x 512 fp32 (LSU requests), this about 2.
+      // the group's i-th. One row per lane took 11.5 us for 128 x 512 fp32 (LSU requests), this 5.5.
       const int row0 = rg * kRows + 32 * quarter + (lane & ~7);
       const size_t qrow0 = (size_t)sg.b * a.rows + row0, prow0 = (size_t)(w + sg.b) * a.rows + row0;
       const bool bf16_out = direct && a.out_dtype == kBF16;

@@ -437,8 +437,8 @@ cudaError_t launch_simt_decode(const DecodeArgs& a, cudaStream_t s) {
   if (chunk > 32) chunk = 32;
   if (chunk < 1) chunk = 1;
   dim3 grid(a.W, (a.rows + kWarps - 1) / kWarps);
-  // the registers of the widest shapes, or of those up to 128 wide (a tiny window of 24-wide rows:
-  // 57 us with 40 + 32 registers and one token at a time, 8 us like this)
+  // the registers of the widest shapes, or of those up to 128 wide (a call on a tiny window of 24-wide rows:
+  // 57 us with 40 + 32 registers and one token at a time; 20 us like this, which the host takes to launch it)
   constexpr int kWQ = kSimtMaxD / 32, kWA = kSimtMaxR / 32;
   auto kernel = D <= 128 ? (a.window > 0 ? simt_decode_kernel<true, 4, 4> : simt_decode_kernel<false, 4, 4>)
                          : (a.window > 0 ? simt_decode_kernel<true, kWQ, kWA> : simt_decode_kernel<false, kWQ, kWA>);

@@ -10,6 +10,9 @@
 // All sums are fp64: the weights are fp32 or bf16 and the draw has to fall on the same token
 // whatever the order of the sum, so its rounding must be far below a weight. Every CTA adds in the
 // same order (chunk, prefix of chunks, prefix of CTAs): the result does not vary between runs.
+// Bound: the reads where the batch is large (128 sequences of 128000 fp32 values in 28 us, 4.7 TB/s;
+// conversions and fp64 sums keep 44 % of the issue slots busy), the chain of dependent loads where it
+// is small (one sequence of 32000 in 11 us of device time).
 #include <type_traits>
 
 #include "mla_device.cuh"
@@ -356,7 +359,8 @@ extern "C" mla_status_t mla_verify_drafts(const mla_verify_params_t* p, const vo
   const bool vec = (size_t)p->vocab * e % 16 == 0 && ((uintptr_t)target | (uintptr_t)draft) % 16 == 0;
   // CTAs per sequence: one per 4096 values (what 8 warps load at once), up to 8, but no more than it
   // takes to give every SM two: a longer slice hides the chain of dependent loads before it (128
-  // sequences of 128000 values: 40 us with 8, 35 us with 4, 41 us with 2)
+  // sequences of 128000 values, the weights still summed with their checks: 40 us with 8, 35 us with 4, 41 us
+  // with 2; 28 us with 4 since)
   int dev = 0, sms = 0, C = 1;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return MLA_ERR_CUDA;
