@@ -267,3 +267,31 @@ def test_a_large_batch_of_short_and_empty_sequences():
         out, lse, st = run(hide(inp, 90, 3), 90, 3)
         assert st == 0
         close(out, lse, R.window(inp, 90, 3))
+
+
+# Every way to cut the tile lists among the workers: evenly, whole sequences (one or more per worker) and parts of
+# a sequence, with more parts than a short or empty sequence has tiles.
+@pytest.mark.parametrize("w", [BF16.with_(B=4, seq_lens=(0, 3000, 2500, 70)), MTP.with_(B=3, seq_lens=(2600, 1, 1900)),
+                               FP8.with_(B=3, seq_lens=(2700, 130, 2200)), BF16.with_(B=2, H=24, seq_lens=(2200, 2600))],
+                         ids=["bf16", "two-row-groups", "fp8", "few-rows"])
+@pytest.mark.parametrize("win,sinks", [(1700, 70), (90, 1)])
+def test_every_cut_of_the_tile_lists(w, win, sinks):
+    inp = W.make_inputs(w)
+    ref, hidden = R.window(inp, win, sinks), hide(inp, win, sinks)
+    for workers in (0, 1, 3, 8, 13, 30, 37):
+        out, lse, st = run(hidden, win, sinks, num_workers=workers)
+        assert st == 0
+        close(out, lse, ref, f"W={workers}")
+
+
+def test_a_bad_block_in_one_part_poisons_the_whole_sequence():
+    w = BF16.with_(B=2, seq_lens=(2600, 2700))
+    inp = W.make_inputs(w)
+    ref = R.window(inp, 2000, 4)
+    for tile in (0, 12, 24, 40):   # the sinks' block, and blocks of different parts of the window
+        bad = dict(inp, block_table=inp["block_table"].copy())
+        bad["block_table"][1, tile] = inp["num_blocks"]
+        out, lse, st = run(bad, 2000, 4)
+        assert st == 6   # MLA_ERR_BAD_BLOCK_ID
+        assert bool(out[1].isnan().all()) and bool(lse[1].isnan().all())
+        close(out[:1], lse[:1], tuple(x[:1] for x in ref), f"tile {tile}")
