@@ -93,15 +93,16 @@ __device__ __forceinline__ int worker_of_tile(long long x, long long T, int W) {
 //     blocks of tokens [0, min(sinks, L)), then those of [lo, L), lo = the first token of the
 //     first row's window. Tile i is block i before the gap and i + gap behind it.
 struct DenseTiles {
+  static constexpr bool kCuts = false;   // never aligned to sequences (see cut() below)
   int bs;
   __device__ __forceinline__ DenseTiles(int bs_) : bs(bs_) {}
   __device__ __forceinline__ int count(int Lc) const { return tiles_of(Lc, bs); }
   __device__ __forceinline__ int block(int i, int) const { return i; }
   __device__ __forceinline__ int gap(int) const { return 0; }
-  __device__ __forceinline__ int cut(long long, int, int, int, int) const { return 0; }
 };
 
 struct WindowTiles {
+  static constexpr bool kCuts = true;
   int bs, Sq, causal, window, sinks, aligned;
   __device__ __forceinline__ WindowTiles(const DecodeArgs& a)
       : bs(a.bs), Sq(a.Sq), causal(a.causal), window(a.window), sinks(a.sinks), aligned(a.aligned) {}
@@ -192,20 +193,23 @@ __device__ __forceinline__ WorkerPlan warp_plan(const int32_t* __restrict__ seq_
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) T += __shfl_xor_sync(0xffffffffu, T, o);
-  most = __reduce_max_sync(0xffffffffu, most);
   WorkerPlan p;
   p.T = T;
   p.W = (T > 0 && T < W) ? (int)T : W;
-  hidden = __reduce_max_sync(0xffffffffu, hidden);
-  p.cut = tiles.cut(T, most, hidden, B, W);
-  if (p.cut) {
-    const int parts = max(-p.cut, 1), k = max(p.cut, 1);   // one of them is 1
-    p.W = W;
-    p.b0 = (int)min((long long)(w / parts) * k, (long long)B);
-    p.start = w % parts;
-    p.P0 = 0;
-    p.end = min((long long)(w / parts + 1) * k, (long long)B);
-    return p;
+  p.cut = 0;
+  if constexpr (Tiles::kCuts) {
+    most = __reduce_max_sync(0xffffffffu, most);
+    hidden = __reduce_max_sync(0xffffffffu, hidden);
+    p.cut = tiles.cut(T, most, hidden, B, W);
+    if (p.cut) {
+      const int parts = max(-p.cut, 1), k = max(p.cut, 1);   // one of them is 1
+      p.W = W;
+      p.b0 = (int)min((long long)(w / parts) * k, (long long)B);
+      p.start = w % parts;
+      p.P0 = 0;
+      p.end = min((long long)(w / parts + 1) * k, (long long)B);
+      return p;
+    }
   }
   p.start = (T > 0 && w < p.W) ? (long long)w * T / p.W : T;
   p.end = (T > 0 && w < p.W) ? (long long)(w + 1) * T / p.W : T;
@@ -266,19 +270,21 @@ struct SegmentIterT {
       : seq_lens(sl), tiles(t), B(B_), cap(cap_), W(plan.W), w(w_), status(st), p(plan), b(plan.b0), P(plan.P0) {}
 
   __device__ bool next(Segment& sg) {
-    while (p.cut && b < (int)p.end) {
-      sg.Lc = clamp_len(__ldg(seq_lens + b), cap, status);
-      sg.b = b++;
-      const int n = tiles.count(sg.Lc);
-      sg.split = (int)p.start;
-      sg.first_worker = w - sg.split;
-      sg.splits = min(max(-p.cut, 1), n);
-      if (sg.split >= sg.splits) continue;   // (no tile at all among them)
-      sg.tile_begin = (int)((long long)n * sg.split / sg.splits);
-      sg.tile_end = (int)((long long)n * (sg.split + 1) / sg.splits);
-      return true;
+    if constexpr (Tiles::kCuts) {
+      while (p.cut && b < (int)p.end) {
+        sg.Lc = clamp_len(__ldg(seq_lens + b), cap, status);
+        sg.b = b++;
+        const int n = tiles.count(sg.Lc);
+        sg.split = (int)p.start;
+        sg.first_worker = w - sg.split;
+        sg.splits = min(max(-p.cut, 1), n);
+        if (sg.split >= sg.splits) continue;   // (no tile at all among them)
+        sg.tile_begin = (int)((long long)n * sg.split / sg.splits);
+        sg.tile_end = (int)((long long)n * (sg.split + 1) / sg.splits);
+        return true;
+      }
+      if (p.cut) return false;
     }
-    if (p.cut) return false;
     while (b < B && P < p.end) {
       const int Lc = clamp_len(__ldg(seq_lens + b), cap, status);
       const int n = tiles.count(Lc);

@@ -391,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, 2) combine_kernel(const DecodeArgs a
   const float qnan = __uint_as_float(0x7FC00000u);
   const long long n = raw < 0 || raw > cap ? 0 : tiles.count(raw);
   int first = 0, splits = 0;
-  const int cut = tiles.cut(total, most, hidden, a.B, a.W);
+  int cut = 0;
+  if constexpr (kWindow) cut = tiles.cut(total, most, hidden, a.B, a.W);
   if (n > 0 && cut) {
     const int parts = max(-cut, 1);
     first = b * parts;

@@ -562,7 +562,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
     const uint32_t rxp = smem_u32(smem + G::kOffRxP), txp = smem_u32(smem + G::kOffTxP);
     const uint32_t alpha_off = kRxPAlpha + orow * 4;
     const int grow = rg * kRows + row;
-    const int grow0 = rg * kRows + lbase + (lane & 8);   // query row of this group of eight lanes' first row
     const bool valid_row = grow < a.rows;
     const int s_idx = valid_row ? grow / a.H : 0;
     const float scale_log2 = a.scale_log2;
@@ -620,27 +619,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
       ok = wait_local(smem_u32(&ctl.q_empty), (seg & 1) ^ 1);
       if (!ok) break;
       {
-        // eight lanes read 128 bytes of a row side by side, then the pieces move to the row's own lane
+        // (One row per lane. By whole lines, as the split-role kernel reads, the exchange's registers spill here:
+        // a step of the 128-head e4m3 cache took 1.71 ms, like this 1.56.)
         uint32_t qv[64];
-        const uint16_t* src = (const uint16_t*)a.q_lat + ((size_t)sg.b * a.rows + grow0) * kR + 256 * rank + 128 * hf +
-                              8 * (lane & 7);
-        uint4 piece8[2][8];
+        const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)a.q_lat +
+                                                         ((size_t)sg.b * a.rows + (valid_row ? grow : 0)) * kR +
+                                                         256 * rank + 128 * hf);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            piece8[k][i] = grow0 + i < a.rows ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)i * kR + 64 * k))
-                                              : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          transpose_pieces<8>(piece8[k]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            qv[32 * k + 4 * i] = piece8[k][i].x;
-            qv[32 * k + 4 * i + 1] = piece8[k][i].y;
-            qv[32 * k + 4 * i + 2] = piece8[k][i].z;
-            qv[32 * k + 4 * i + 3] = piece8[k][i].w;
-          }
+        for (int i = 0; i < 16; ++i) {
+          const uint4 v = valid_row ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+          qv[4 * i] = v.x;
+          qv[4 * i + 1] = v.y;
+          qv[4 * i + 2] = v.z;
+          qv[4 * i + 3] = v.w;
         }
         if constexpr (kFp8) {
           // the latent score MMAs take fp16 operands: the bf16 query words to fp16 (exact for
@@ -655,8 +646,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
         tc_fence_before();
         mbar_arrive(smem_u32(&ctl.q_full));
       }
-      // (here, while the first tile is scored: its loads would hold the epilogue up)
-      const bool poisoned = segment_poisoned(a, tiles, sg.b, sg.tile_begin, sg.tile_end);
       const int n = sg.tile_end - sg.tile_begin;
       const int last_tile = tiles.count(sg.Lc) - 1;
       float m_run = -INFINITY, l_run = 0.f;   // own rows: running maximum (log2 units), this thread's sum
@@ -933,57 +922,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_for<kFp8, kS
         __syncwarp();
         if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.lrx_full[seg & 1]), kLrxBytes);   // segment seg + 2
       }
+      const bool poisoned = segment_poisoned(a, tiles, sg.b, sg.tile_begin, sg.tile_end);
       const float inv = poisoned ? __uint_as_float(0x7FC00000u) : l_tot > 0.f ? 1.f / l_tot : 0.f;
       const size_t qrow = (size_t)sg.b * a.rows + grow;
       const bool direct = sg.splits == 1;
       const size_t prow = (size_t)(w + sg.b) * a.rows + grow;
-      // Eight lanes write 128 bytes of a row side by side: the row of instruction i is the group's i-th.
-      const size_t qrow0 = (size_t)sg.b * a.rows + grow0, prow0 = (size_t)(w + sg.b) * a.rows + grow0;
-      const int ch0 = 256 * (int)rank + 128 * hf;
-      // 16 columns of this row, times 1 / l, as fp32 pieces u[0..3] or bf16 pieces u[0..1]
-      auto load16 = [&](int c, uint4* u, bool bf16) {
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
         uint32_t v[16];
         tmem_ld16x2<128>(tmem + lane_off + kTmemO + 16 * c, v);
         tmem_wait_ld();
-        float f[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]) * inv;
-        if (bf16) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            u[i] = make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]), pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
-                              pack_bf16x2(f[8 * i + 4], f[8 * i + 5]), pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
+        if (!valid_row) continue;
+        const int ch = 256 * (int)rank + 128 * hf + 16 * c;
+        if (direct && a.out_dtype == kBF16) {
+          uint4 o0, o1;
+          o0.x = pack_bf16x2(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv);
+          o0.y = pack_bf16x2(__uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv);
+          o0.z = pack_bf16x2(__uint_as_float(v[4]) * inv, __uint_as_float(v[5]) * inv);
+          o0.w = pack_bf16x2(__uint_as_float(v[6]) * inv, __uint_as_float(v[7]) * inv);
+          o1.x = pack_bf16x2(__uint_as_float(v[8]) * inv, __uint_as_float(v[9]) * inv);
+          o1.y = pack_bf16x2(__uint_as_float(v[10]) * inv, __uint_as_float(v[11]) * inv);
+          o1.z = pack_bf16x2(__uint_as_float(v[12]) * inv, __uint_as_float(v[13]) * inv);
+          o1.w = pack_bf16x2(__uint_as_float(v[14]) * inv, __uint_as_float(v[15]) * inv);
+          uint4* dst = reinterpret_cast<uint4*>((uint16_t*)a.out + qrow * kR + ch);
+          dst[0] = o0;
+          dst[1] = o1;
         } else {
+          float* dst = direct ? (float*)a.out + qrow * kR + ch : a.o_part + prow * kR + ch;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            u[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
-                              __float_as_uint(f[4 * i + 3]));
-        }
-      };
-      if (direct && a.out_dtype == kBF16) {
-#pragma unroll 1
-        for (int c = 0; c < 8; c += 4) {
-          uint4 u[8];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) load16(c + h, u + 2 * h, true);
-          transpose_pieces<8>(u);
-          uint16_t* dst = (uint16_t*)a.out + qrow0 * kR + ch0 + 16 * c + 8 * (lane & 7);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (grow0 + i < a.rows) *reinterpret_cast<uint4*>(dst + (size_t)i * kR) = u[i];
-        }
-      } else {
-        float* base = direct ? (float*)a.out + qrow0 * kR : a.o_part + prow0 * kR;
-#pragma unroll 1
-        for (int c = 0; c < 8; c += 2) {
-          uint4 u[8];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) load16(c + h, u + 4 * h, false);
-          transpose_pieces<8>(u);
-          float* dst = base + ch0 + 16 * c + 4 * (lane & 7);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (grow0 + i < a.rows) *reinterpret_cast<uint4*>(dst + (size_t)i * kR) = u[i];
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4*>(dst + i) =
+                make_float4(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv,
+                            __uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
         }
       }
       if (own && hf == 0 && valid_row) {
