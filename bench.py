@@ -79,7 +79,7 @@ def load_peaks():
 # only holds for the sources the kernel was built from, keyed here by kernel and the SHA-256 prefix of
 # those files; for any other source the bench reports traffic as null.
 MEASURED_TRAFFIC = {
-    ("tc_pair", "c34dd76ad94899ec"): {"deepseek_v3": (304.350976e6 + 4.457728e6) / 262144},
+    ("tc_pair", "b42f8e88e411e882"): {"deepseek_v3": (304.367872e6 + 5.932544e6) / 262144},
 }
 KERNEL_SOURCES = {
     "tc_pair": ("mla_pair.cu", "ptx_sm100.cuh", "mla_device.cuh", "mla_internal.h", "mla_tc.h"),
@@ -88,7 +88,7 @@ KERNEL_SOURCES = {
 # The same for the sparse step's indexer (dram bytes per context token, batch 8 of the
 # 128K workload), keyed by the sources of mla_dsa.cu and its headers.
 DSA_TRAFFIC = {
-    "9f69c58ab496e496": {"dsa_v32": (138.620416e6 + 4.136448e6) / (8 * 131072)},
+    "1d72216b1b3fb8f4": {"dsa_v32": (138.622720e6 + 4.129280e6) / (8 * 131072)},
 }
 DSA_SOURCES = ("mla_dsa.cu", "ptx_sm100.cuh", "mla_device.cuh", "mla_internal.h")
 

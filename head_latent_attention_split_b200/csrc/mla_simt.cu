@@ -449,7 +449,7 @@ cudaError_t launch_simt_decode(const DecodeArgs& a, cudaStream_t s) {
 
 cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t s) {
   // Blocks for two per SM: a block finds its sequence's splits once and walks its rows. (With one block per eight
-  // rows, the 3072 blocks of 96 sequences x 256 rows with nothing to merge took 49 us by themselves.)
+  // rows, 64 sequences x 128 rows with nothing to merge took 12.6 us by themselves, like this 4.6.)
   constexpr int kSms = 148;
   const int groups = (a.rows + kWarps - 1) / kWarps;
   dim3 grid(a.B, std::max(1, std::min(groups, 2 * kSms / std::max(a.B, 1))));
