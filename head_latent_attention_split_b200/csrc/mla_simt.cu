@@ -190,7 +190,9 @@ __global__ void __launch_bounds__(kThreads) simt_decode_kernel(const DecodeArgs 
 }
 
 // One row's output and log-sum-exp from its `splits` partials (not 1), by one warp; none: zeros, or NaN behind a
-// length that is out of range.
+// length that is out of range. kMany: many rows per warp slot, where resident warps hide the latencies; else the
+// first partials are requested before their weights are known.
+template <bool kMany>
 __device__ __forceinline__ void combine_row(const DecodeArgs& a, int b, int row, int first, int splits, bool bad) {
   const int lane = threadIdx.x & 31;
   const size_t orow = (size_t)b * a.rows + row;
@@ -203,9 +205,10 @@ __device__ __forceinline__ void combine_row(const DecodeArgs& a, int b, int row,
   const size_t slot0 = (size_t)first + b;
   const bool vec = a.r % 4 == 0;
   // the first two splits' pieces of the first 512 channels (see below), requested at once
+  constexpr int kEarly = kMany ? 0 : 2;
   float4 early[2][4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < kEarly; ++i) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int k = 4 * lane + 128 * u;
@@ -261,15 +264,15 @@ __device__ __forceinline__ void combine_row(const DecodeArgs& a, int b, int row,
       int i0 = 0;
       if (k0 == 0) {   // (splits >= 2)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kEarly; ++i) {
           const float wgt = __shfl_sync(0xffffffffu, wl, i);
           if (wgt != 0.f) add(wgt, early[i]);
         }
-        i0 = 2;
+        i0 = kEarly;
       }
       // splits whose pieces are on their way together, added in order (1 sequence of 65 tiles in 17 parts: 36.0 us
       // with 2, 37.0 with 3, 38.2 with 4, whose registers spill)
-      constexpr int kG = 2;
+      constexpr int kG = kMany ? 1 : 2;
 #pragma unroll 1
       for (int i = i0; i < splits; i += kG) {
         float4 v[kG][4];
@@ -346,8 +349,8 @@ __device__ __forceinline__ void combine_row(const DecodeArgs& a, int b, int row,
 // window decode launches it as a dependent of the decode kernel, with the lengths read and the
 // split found while that kernel still runs, and the partials of the first splits are requested before
 // their weights are known.
-template <bool kWindow>
-__global__ void __launch_bounds__(kThreads, 2) combine_kernel(const DecodeArgs a) {
+template <bool kWindow, bool kMany>
+__global__ void __launch_bounds__(kThreads, kMany ? 4 : 2) combine_kernel(const DecodeArgs a) {
   __shared__ long long s_sum[kWarps][2];
   __shared__ int s_most[kWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 2) combine_kernel(const DecodeArgs a
   if constexpr (kWindow) ptx::wait_for_grid_before();   // every thread, so that this grid ends after the decode's
   if (splits == 1) return;                              // (the decode wrote the rows directly)
   for (int row = blockIdx.y * kWarps + warp; row < a.rows; row += gridDim.y * kWarps)
-    combine_row(a, b, row, first, splits, raw < 0 || raw > cap);
+    combine_row<kMany>(a, b, row, first, splits, raw < 0 || raw > cap);
 }
 
 __global__ void __launch_bounds__(32) plan_probe_kernel(const DecodeArgs a, int32_t* token_slot,
@@ -448,11 +451,16 @@ cudaError_t launch_simt_decode(const DecodeArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t s) {
-  // Blocks for two per SM: a block finds its sequence's splits once and walks its rows. (With one block per eight
-  // rows, 64 sequences x 128 rows with nothing to merge took 12.6 us by themselves, like this 4.6.)
+  // Up to two blocks per SM with one per eight rows: latency decides (32 e4m3 window sequences of 34 tiles: 72.5 us,
+  // 75.0 with the other variant at three per SM). Beyond, occupancy does: 128 x 256 rows of a ragged batch
+  // merge in 24.6 us with 61 registers, 36.9 with 118. A dense batch then keeps a block per eight rows, since its
+  // sequences' splits differ (30.7 us when four per SM walk the rows); the blocks of a window batch walk
+  // them, since its splits are alike and often single (133 us a step, 141 otherwise).
   constexpr int kSms = 148;
-  const int groups = (a.rows + kWarps - 1) / kWarps;
-  dim3 grid(a.B, std::max(1, std::min(groups, 2 * kSms / std::max(a.B, 1))));
+  const int groups = (a.rows + kWarps - 1) / kWarps, batch = std::max(a.B, 1);
+  const bool many = (int64_t)groups * batch > 2 * kSms;
+  const int walk = std::max(1, std::min(groups, (many ? 4 : 2) * kSms / batch));
+  const dim3 grid(a.B, many && a.window == 0 ? groups : walk);
   if (a.window > 0) {
     // a dependent of the decode kernel before it: its blocks may start while that kernel's last CTAs run
     cudaLaunchConfig_t cfg{};
@@ -464,9 +472,12 @@ cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t s) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, combine_kernel<true>, a);
+    return many ? cudaLaunchKernelEx(&cfg, combine_kernel<true, true>, a) : cudaLaunchKernelEx(&cfg, combine_kernel<true, false>, a);
   }
-  combine_kernel<false><<<grid, kThreads, 0, s>>>(a);
+  if (many)
+    combine_kernel<false, true><<<grid, kThreads, 0, s>>>(a);
+  else
+    combine_kernel<false, false><<<grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
