@@ -63,6 +63,16 @@ def test_select_matches_a_sort(kind, S, lens, budget, sinks, recent):
     np.testing.assert_array_equal(idx, ref_i)
 
 
+@pytest.mark.parametrize("kind", ["lognormal", "ties", "special"])
+@pytest.mark.parametrize("S", [4095, 4096, 4097, 8191, 8192, 8193])
+def test_select_around_the_rows_that_change_the_keys_per_thread(kind, S):
+    lens = (S, S - 1, S - 5, 1025)
+    mass = masses(kind, len(lens), S, seed=S)
+    idx, cnt, st = select(mass, lens, 1024, 3, 200)
+    ref_i, ref_c = R.evict(mass, lens, 1024, 3, 200)
+    assert st == 0 and np.array_equal(idx, ref_i) and np.array_equal(cnt, ref_c)
+
+
 def test_select_rows_longer_than_a_cluster_holds():
     S = 8 * 16384 * 2 + 77
     mass = masses("ties", 2, S, 3) + masses("lognormal", 2, S, 4).round(1)

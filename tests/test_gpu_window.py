@@ -295,3 +295,11 @@ def test_a_bad_block_in_one_part_poisons_the_whole_sequence():
         assert st == 6   # MLA_ERR_BAD_BLOCK_ID
         assert bool(out[1].isnan().all()) and bool(lse[1].isnan().all())
         close(out[:1], lse[:1], tuple(x[:1] for x in ref), f"tile {tile}")
+
+
+def test_a_large_batch_with_one_long_window():
+    w = BF16.with_(B=80, H=32, seq_lens=(6000,) + tuple(1 + 7 * i for i in range(79)))   # an even cut, many rows to merge
+    inp = W.make_inputs(w)
+    out, lse, st = run(hide(inp, 5500, 3), 5500, 3)
+    assert st == 0
+    close(out, lse, R.window(inp, 5500, 3))
