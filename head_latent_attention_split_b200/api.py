@@ -214,6 +214,8 @@ def _dims(t, what, n):
     s = t.shape
     if len(s) != n:
         raise ValueError(f"{what} must have {n} dimensions, got {len(s)}")
+    if t.numel() >= 2 ** 31 and max(s) >= 2 ** 31:
+        raise ValueError(f"{what}: shape {tuple(s)}, a dimension does not fit 32 bits")
     return s
 
 
@@ -248,8 +250,8 @@ def _step(q_lat, q_rope, kv_cache, block_table, seq_lens, softmax_scale, causal,
     qd = _b.BF16 if cd == _b.E4M3 else cd
     if out_dtype is None:
         out_dtype = qd
-    return dev, _b.Params(B, Sq, H, r, d_r, bs, nb, mb, qd, cd, out_dtype, 1 if causal else 0, softmax_scale, num_workers,
-                          _b.KERNELS[kernel] if isinstance(kernel, str) else kernel, 0)
+    return dev, _b.Params(B, Sq, H, r, d_r, bs, nb, mb, qd, cd, out_dtype, 1 if causal else 0, softmax_scale,
+                          _b.int32(num_workers, "num_workers"), _b.KERNELS[kernel] if isinstance(kernel, str) else kernel, 0)
 
 
 _workspace_bytes = {}   # (device, parameters) -> mla_decode_workspace_size, a function of nothing else
@@ -334,6 +336,7 @@ def evict_select(mass, seq_lens, budget, sinks=0, recent=0, indices=None, counts
     dev = _cuda_device(mass, "mass")
     B, S = _dims(mass, "mass", 2)
     i32 = torch.int32
+    budget, sinks, recent = _b.int32(budget, "budget"), _b.int32(sinks, "sinks"), _b.int32(recent, "recent")
     _need(dev, "mass", mass, torch.float32, (B, S))
     _need(dev, "seq_lens", seq_lens, i32, (B,))
     if indices is not None:

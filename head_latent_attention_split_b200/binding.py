@@ -7,6 +7,7 @@ library is loaded on first use, and a missing or stale library raises then.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import numpy as np
@@ -35,6 +36,14 @@ class MlaError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
         super().__init__(f"{where}: {STATUS.get(status, status)}")
+
+
+def int32(x, what: str) -> int:
+    """x as an integer of 32 bits, or an error: ctypes would cut it to its low bits."""
+    x = operator.index(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{what} = {x} does not fit 32 bits")
+    return x
 
 
 class Params(ctypes.Structure):
@@ -375,7 +384,7 @@ def mla_window_decode(p: Params, window: int, sinks: int, q_lat, q_rope, kv_cach
     """Raw C-ABI call of the decode over a sliding window and sink tokens."""
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = lib.mla_window_decode(ctypes.byref(p), int(window), int(sinks), _addr(q_lat), _addr(q_rope), _addr(kv_cache),
+    st = lib.mla_window_decode(ctypes.byref(p), int32(window, "window"), int32(sinks, "sinks"), _addr(q_lat), _addr(q_rope), _addr(kv_cache),
                                _addr(k_rope_cache), _addr(kv_scale), _addr(block_table), _addr(seq_lens), _addr(out),
                                _addr(lse), _addr(workspace), workspace_bytes, _stream(stream))
     if check:
@@ -386,7 +395,7 @@ def mla_window_decode(p: Params, window: int, sinks: int, q_lat, q_rope, kv_cach
 def mla_attention_mass(p: Params, max_seq_len: int, q_lat, q_rope, kv_cache, k_rope_cache, kv_scale, block_table,
                        seq_lens, lse, mass_in, mass, stream=None, check=True) -> int:
     """Raw C-ABI call of the attention weight per cached token."""
-    st = lib.mla_attention_mass(ctypes.byref(p), int(max_seq_len), _addr(q_lat), _addr(q_rope), _addr(kv_cache),
+    st = lib.mla_attention_mass(ctypes.byref(p), int32(max_seq_len, "max_seq_len"), _addr(q_lat), _addr(q_rope), _addr(kv_cache),
                                 _addr(k_rope_cache), _addr(kv_scale), _addr(block_table), _addr(seq_lens), _addr(lse),
                                 _addr(mass_in), _addr(mass), _stream(stream))
     if check:

@@ -48,6 +48,13 @@ def test_window_decode_refusals(m, bad, code):
     assert _window(m, **bad) == code
 
 
+@pytest.mark.parametrize("call", [lambda m: _window(m, window=2 ** 32 + 16), lambda m: _window(m, sinks=2 ** 32),
+                                  lambda m: _mass(m, max_seq_len=2 ** 32 + 64)])
+def test_numbers_beyond_32_bits_are_refused_not_cut(m, call):
+    with pytest.raises(ValueError, match="32 bits"):
+        call(m)
+
+
 def _mass(m, **kw):
     ptrs, kw = _split(dict(DECODE_PTRS, lse=FAKE, mass_in=None, mass=FAKE), dict(kw))
     S = kw.pop("max_seq_len", 64)

@@ -250,3 +250,12 @@ def test_select_and_compact_in_a_graph():
         j = torch.arange(ref_c[b], device="cuda")
         assert torch.equal(flat[dt[b, j // bs].long() * bs + j % bs], flat[bt[b, t // bs].long() * bs + t % bs])
         assert torch.equal(out[b, :ref_c[b]], mass[b, t]) and bool((out[b, ref_c[b]:] == 0).all())
+
+
+@pytest.mark.parametrize("bad", [dict(budget=2 ** 32 + 8), dict(sinks=2 ** 32), dict(recent=-2 ** 32 + 2)])
+def test_select_numbers_beyond_32_bits_are_refused_not_cut(bad):
+    import torch
+    import head_latent_attention_split_b200 as mla
+    mass, lens = torch.ones(2, 40, device="cuda"), torch.tensor([40, 30], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="32 bits"):
+        mla.evict_select(mass, lens, **{**dict(budget=8, sinks=1, recent=2), **bad})
