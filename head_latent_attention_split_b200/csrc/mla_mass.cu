@@ -22,7 +22,7 @@
 // Bound: memory. Per 128 tokens and SM 36 MMAs of N = 128 take about 2.9 k cycles and the
 // exponentials about 1.1 k (16 per cycle), the tile's bytes at 1/148 of the HBM rate 6.4 k (bf16)
 // or 3.6 k (e4m3). Measured at 128 heads: bf16, 64 sequences of 8192: 111 us (5.4 TB/s; up to 124 us in long
-// runs under the power cap); e4m3, 48 sequences of up to 16384: 66 us (2.7 TB/s). What is missing is
+// runs under the power cap); e4m3, 48 sequences of up to 16384: 63 us (2.9 TB/s). What is missing is
 // the ring: 80 KB in flight per SM beside the query, at about 2.2 us of latency under load, and with an
 // e4m3 cache the start of each sequence's tiles behind its query. An L2 prefetch of the blocks ahead made it
 // slower (117 to 122 us and more), other L2 promotion sizes changed nothing.
@@ -246,6 +246,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int slot = 0, issued = 0;
       uint32_t phase = 0, item = 0, u = 0, q_issued = 0;   // u: tiles; q_issued: query chunks loaded so far
       const bool ok = for_items([&](int b, int Lc, int g, int t0, int t1) {
+        if constexpr (kFp8)   // the sum warps' reads of the item's query, a ring's time early (64.9 us without, 63.1)
+          prefetch_l2((const uint16_t*)a.q_lat + ((size_t)b * a.rows + g * kGroupRows) * kR,
+                      (uint32_t)min(a.rows - g * kGroupRows, kGroupRows) * kR * 2);
         const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
         const int blocks = tiles_of(Lc, kBS);
         int next[2] = {__ldg(bt + 2 * t0), 2 * t0 + 1 < blocks ? __ldg(bt + 2 * t0 + 1) : 0};
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if constexpr (kFp8) {
         // the group's query in two terms. Its last readers were the previous item's MMAs, and their last
         // sums are done.
-        constexpr int kU = 4;   // rows in flight per warp
+        constexpr int kU = 4;   // rows in flight per warp (8, or 4 ahead of 4: registers and code, slower)
         for (int r0 = kU * warp; r0 < N; r0 += 8 * kU) {
           uint4 v[kU][2];
 #pragma unroll
