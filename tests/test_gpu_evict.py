@@ -259,3 +259,32 @@ def test_select_numbers_beyond_32_bits_are_refused_not_cut(bad):
     mass, lens = torch.ones(2, 40, device="cuda"), torch.tensor([40, 30], dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError, match="32 bits"):
         mla.evict_select(mass, lens, **{**dict(budget=8, sinks=1, recent=2), **bad})
+
+
+def test_back_to_back_selections_and_copies_see_each_others_writes():
+    import torch
+    import head_latent_attention_split_b200 as mla
+    g = torch.Generator(device="cuda").manual_seed(5)
+    B, S, bs, budget = 40, 1000, 64, 300
+    mb, db = 16, 5
+    perm = torch.randperm(B * (mb + db), generator=g, device="cuda").int()
+    bt, dt = perm[:B * mb].reshape(B, mb).contiguous(), perm[B * mb:].reshape(B, db).contiguous()
+    kv = torch.empty(B * (mb + db), bs, 576, dtype=torch.bfloat16, device="cuda")
+    idx, cnt = torch.empty(B, budget, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+    out, lens = torch.empty(B, budget, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    j = torch.arange(budget, device="cuda")
+    for i in range(40):   # nothing waits on the host in between; every buffer is used again
+        kv.normal_(generator=g)
+        mass = torch.rand(B, S, generator=g, device="cuda")
+        lens.random_(200, S + 1, generator=g)
+        mla.evict_select(mass, lens, budget, 4, 50, indices=idx, counts=cnt)
+        mla.cache_compact(kv, bt, dt, idx, cnt, mass=mass, mass_out=out)
+        t = idx.long().clamp(min=0)
+        src = (bt.gather(1, t // bs).long() * bs + t % bs)
+        dst = dt[:, j // bs].long() * bs + j % bs
+        live = j < cnt[:, None]
+        flat = kv.view(-1, 576)
+        wrong += ((flat[src] != flat[dst]).any(-1) & live).sum() + ((out != mass.gather(1, t)) & live).sum()
+        wrong += (cnt != lens.clamp(max=budget)).sum() + ((idx >= 0) != live).sum()
+    assert int(wrong) == 0 and mla.device_status() == 0
