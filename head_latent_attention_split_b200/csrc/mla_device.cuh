@@ -59,6 +59,19 @@ __device__ __forceinline__ void split_e4m3(uint32_t v0, uint32_t v1, float down,
   lo = f32x2_to_e4m3(x0 - h0, x1 - h1) | (f32x2_to_e4m3(x2 - h2, x3 - h3) << 16);
 }
 
+// Two e5m2 codes (2 mantissa bits, normal from 2^-14, smallest step 2^-16).
+__device__ __forceinline__ uint32_t f32x2_to_e5m2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The number c for which (x + c) - c is x to the nearest e4m3 value (|x| below 448): 1.5 * 2^20 times the
+// power of two at or below |x|, or times 2^-6, e4m3's smallest normal: c's last place is then that of x's
+// four significant bits, and 2^-9 for smaller x.
+__device__ __forceinline__ float e4m3_rounder(float x) {
+  return __uint_as_float(max(__float_as_uint(x) & 0x7F800000u, 121u << 23) + ((20u << 23) | 0x400000u));
+}
+
 __device__ __forceinline__ float load_q(const void* p, int dtype, size_t i) {
   return dtype == kF32 ? __ldg((const float*)p + i) : bf16_bits_to_float(__ldg((const uint16_t*)p + i));
 }

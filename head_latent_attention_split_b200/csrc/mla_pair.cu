@@ -42,10 +42,20 @@
 //     shared memory) have a second one, since a token's scale applies to the latent part only:
 //     score = 2^e (acc s_t + rope), the query's power of two in the row's softmax scale. 36 MMAs per tile pair,
 //     as with a bf16 cache.
-//   probabilities: P s_t as two e4m3 terms (2^-8, a bf16 rounding's accuracy), so the PV is 8 MMAs per
-//     tile on the codes themselves. The running maximum is that of score + log2 s_t, the logarithm of
-//     what P holds, and its reference sits 2^4 below it: P s_t stays in [0, 2^8], and e4m3's smallest
-//     step (2^-9, of which both terms may lose half) costs at most 2^-13 of the largest term.
+//   probabilities: w = P s_t as hi = e4m3(w) and lo = e5m2(w - hi), the remainder behind the stored hi, so the
+//     PV is 8 MMAs per tile on the codes themselves. The remainder of 4 significant bits is at most half of
+//     the fourth one, and e5m2's three hold it to 2^-8 of w, a bf16 rounding's accuracy, from e4m3's smallest
+//     normal 2^-6 upward; a smaller w is off by 2^-14 at most (remainders up to half of e4m3's step 2^-9).
+//     What that loses must stay small against the row's sum however many tokens there are (a sink that holds
+//     half of it leaves every other token 2^-14 and less), so the reference of w follows the maximum of score
+//     + log2 s_t, the logarithm of what w holds, up AND down: it is set 2^4 below a pair's maximum when that
+//     exceeds it by 2^8, and again, by the largest of them, when eight pairs of one row stayed below
+//     2^2. Per reference the pairs below 2^2 lose 8 x 128 x 2^-14 = 2^-4 at most, against the token of 2^4
+//     that set it, and any other pair 128 x 2^-14 = 2^-7 against its own maximum of 2^2 or more: together
+//     2^-8 + 2^-9 of the row's sum of w, for any scores and any length. (The reference goes down by 2^24
+//     below its highest at most, so that sums stay finite; what is smaller than that has no weight.)
+//     Down steps cost what the up steps do, a pass over O: at scores of deviation 1.7, 33 pairs make 6 up and
+//     2 down steps per warp.
 //   Half the bytes per tile: twice the ring slots.
 //   Bound by the softmax warps, 3.4 us per tile pair at 128 rows (bf16 2.3): scores and scales 1.05,
 //   exponentials and the two terms 1.15, the message 0.55, the rest waiting; a segment's start costs
@@ -123,7 +133,10 @@ constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kPostWarp = 10;      // score CTA: copies each written message to the output CTA
 constexpr float kRescaleThreshold = 8.0f;
-constexpr float kHeadroom8 = 4.0f;   // e4m3 cache: P s_t starts at 2^4 (and stays below 2^8)
+// e4m3 cache: P s_t starts at 2^4 and stays below 2^8; pairs whose maximum is below 2^2 lower the reference when
+// there are kLowPairs8 of them, to 2^-24 of its highest at most
+constexpr float kHeadroom8 = 4.0f, kLow8 = 2.0f, kDepth8 = 24.0f;
+constexpr int kLowPairs8 = 8;
 constexpr float kScaleFloor = 0x1p-64f;   // of a token's scale, in the running maximum only
 
 struct Ctl {
@@ -492,6 +505,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     while (it.next(sg)) {
       const int n = sg.tile_end - sg.tile_begin;
       float m_run = -INFINITY, l_run = 0.f, l_tot = 0.f;   // l_run: this half's columns
+      float m_top = -INFINITY, low_max = -INFINITY;        // e4m3 cache: highest reference; largest low pair
+      int low = 0;                                         // ... and the number of low pairs under this reference
       bool poisoned = false;
       float scale_log2 = a.scale_log2;   // e4m3 cache: times 2^e, the power of two of this row's query
       if (ok) {
@@ -729,10 +744,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = wait_warp(smem_u32(&ctl.xbar[quarter]), u & 1);   // bounded: the partner warp may have aborted
           if (!ok) break;
           const float mt = fmaxf(mh, ctl.xmax[u & 1][half ^ 1][row]);
-          const bool grow_max = mt > m_run + kRescaleThreshold;
-          const float m_new = kFp8 ? mt - kHeadroom8 : mt;
-          const float alpha = (grow_max && m_run != -INFINITY) ? ex2_approx(m_run - m_new) : 1.f;
-          if (grow_max) {
+          bool move = mt > m_run + kRescaleThreshold;   // the reference moves
+          float m_new = kFp8 ? mt - kHeadroom8 : mt;
+          if constexpr (kFp8) {
+            if (move) {
+              m_top = fmaxf(m_top, m_new);
+            } else if (mt < m_run + kLow8 && mt > -INFINITY && m_run > m_top - kDepth8) {
+              ++low;
+              low_max = fmaxf(low_max, mt);
+            }
+            // one row's turn lowers all of the warp's rows with low pairs (both halves decide alike)
+            if (__any_sync(0xffffffffu, low >= kLowPairs8) && low > 0 && !move) {
+              move = true;
+              m_new = fmaxf(low_max - kHeadroom8, m_top - kDepth8);
+            }
+            if (move) {
+              low = 0;
+              low_max = -INFINITY;
+            }
+          }
+          const float alpha = (move && m_run != -INFINITY) ? ex2_approx(m_run - m_new) : 1.f;
+          if (move) {
             l_run *= alpha;
             m_run = m_new;
           }
@@ -758,10 +790,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   acc = add2(acc, p2);
                   const unsigned long long w2 = mul2(p2, h ? s4.y : s4.x);
                   f2_unpack(w2, w0, w1);
-                  const float h0 = top4(w0), h1 = top4(w1);
-                  f2_unpack(fma2(f2_pack(h0, h1), f2_pack(-1.f, -1.f), w2), l0, l1);
+                  const unsigned long long c2 = f2_pack(e4m3_rounder(w0), e4m3_rounder(w1)), minus = f2_pack(-1.f, -1.f);
+                  const unsigned long long h2 = fma2(c2, minus, add2(w2, c2));   // hi's value
+                  float h0, h1;
+                  f2_unpack(h2, h0, h1);
+                  f2_unpack(fma2(h2, minus, w2), l0, l1);
                   hi[h] = f32x2_to_e4m3(h0, h1);
-                  lo[h] = f32x2_to_e4m3(l0, l1);
+                  lo[h] = f32x2_to_e5m2(l0, l1);
                 }
                 pk[k] = hi[0] | (hi[1] << 16);
                 pk[16 + k] = lo[0] | (lo[1] << 16);
@@ -939,6 +974,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ output CTA: MMA issuer (converged warp)
     const bool leader = elect_one();
     constexpr uint32_t idesc_pv = kFp8 ? idesc_e4m3_f32(128, 256, true) : idesc_bf16_f32(128, 256, true);
+    constexpr uint32_t idesc_lo = idesc_f8_f32(128, 256, true, false, true);   // e4m3 cache: P's lo terms are e5m2
     // A = P[128 rows][16 tokens per step] (K-major); the message's P: 8-row x 16-byte core matrices, 128
     // bytes apart along the rows, 2 KB apart along the tokens
     const uint64_t rx_desc = smem_desc(smem_u32(smem + kOffRx), 2048, 128, kSwizzleNone);
@@ -967,7 +1003,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < 4; ++kk) {
               const uint32_t acc = (li > 0 || kk > 0) ? 1u : 0u;
               if constexpr (kFp8)
-                mma_f8_ss(tmem + 256 * hc, adesc + kk * (4096 >> 4), bdesc + (kk & 1) * (4096 >> 4), idesc_pv, acc);
+                mma_f8_ss(tmem + 256 * hc, adesc + kk * (4096 >> 4), bdesc + (kk & 1) * (4096 >> 4), kk < 2 ? idesc_pv : idesc_lo,
+                          acc);
               else
                 mma_ss(tmem + 256 * hc, adesc + kk * (4096 >> 4), bdesc + kk * (2048 >> 4), idesc_pv, acc);
             }

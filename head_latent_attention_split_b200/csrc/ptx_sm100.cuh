@@ -503,15 +503,20 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, boo
          | ((M >> 4) << 24);
 }
 
-// Instruction descriptor for kind::f8f6f4 with e4m3 A/B (format code 0), A K-major, fp32
-// accumulation.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, bool b_mn_major = false) {
+// Instruction descriptor for kind::f8f6f4 with e4m3 (format code 0) or e5m2 (1) A and B, A K-major,
+// fp32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_f8_f32(uint32_t M, uint32_t N, bool a_e5m2, bool b_e5m2, bool b_mn_major = false) {
   return (1u << 4)                   // D format: f32
-         | (0u << 7)                 // A format: e4m3
-         | (0u << 10)                // B format: e4m3
+         | ((a_e5m2 ? 1u : 0u) << 7)
+         | ((b_e5m2 ? 1u : 0u) << 10)
          | ((b_mn_major ? 1u : 0u) << 16)
          | ((N >> 3) << 17)
          | ((M >> 4) << 24);
+}
+
+// ... with both e4m3.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, bool b_mn_major = false) {
+  return idesc_f8_f32(M, N, false, false, b_mn_major);
 }
 
 }  // namespace ptx

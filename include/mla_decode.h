@@ -375,12 +375,17 @@ mla_status_t mla_sparse_decode(const mla_decode_params_t* params, int32_t top_k,
  *     n_s = seq_lens[b] (causal == 0)  or  seq_lens[b] - Sq + 1 + s (causal != 0),
  * so a row's window holds its last `window` tokens, its own included, and a sink inside the window
  * counts once. window >= 1, sinks >= 0; values past the block table's capacity act as the
- * capacity (a window of at least the sequence's length is mla_decode). out, lse, the other
+ * capacity. A window of at least the sequence's length is mla_decode's definition, and by the same
+ * kernel its result (for an E4M3 cache AUTO takes another one here). out, lse, the other
  * arguments, the workspace (mla_decode_workspace_size of the same params) and the handling of
  * bad lengths and blocks are mla_decode's; the sequences' RoPE keys keep the positions they were
  * rotated for. Kernels: mla_decode's, and MLA_KERNEL_TC_PAIR takes an E4M3 cache too (AUTO's choice
- * for it): the query and the weights then go to the FP8 tensor path as two e4m3 terms each, the query's
- * error at most 2^-16 of its row's largest magnitude (RoPE part included), a weight's 2^-8 as with a bf16 cache. Blocks that hold no token any row sees are not read and
+ * for it): the query and the weights then go to the FP8 tensor path as two 8-bit terms each. The query's
+ * error is at most 2^-16 of its row's largest magnitude (RoPE part included). A weight times its token's scale
+ * is held to 2^-8 of itself, as with a bf16 cache; what is small against its neighbours may lose more, but all
+ * that such weights of a row lose together stays below 2^-8 + 2^-9 of the row's sum, however many they are. (TCGEN05 holds
+ * them as mla_decode does: in fp16, the row's largest weight as 1 to 2^8, so that a weight times its scale
+ * loses bits below 2^-14 and is gone below 2^-25.) Blocks that hold no token any row sees are not read and
  * their block ids are not checked. Tokens that no row of the sequence sees may hold anything (NaN
  * included); a token that some row sees has to be finite, as in mla_decode. */
 mla_status_t mla_window_decode(const mla_decode_params_t* params, int32_t window, int32_t sinks,
