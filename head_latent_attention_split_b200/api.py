@@ -360,7 +360,7 @@ def cache_compact(kv_cache, block_table, dst_block_table, indices, counts, k_rop
                   mass_out=None, stream=None):
     """Copy the listed tokens into the (free) blocks of dst_block_table, in list order (see
     mla_cache_compact): counts are the sequences' lengths under the new table. With mass and mass_out
-    the tokens' weights move along, and the rest of each mass_out row becomes 0. Returns None."""
+    (two buffers) the tokens' weights move along, and the rest of each mass_out row becomes 0. Returns None."""
     import torch
     dev = _cuda_device(kv_cache, "kv_cache")
     nb, bs, width = _dims(kv_cache, "kv_cache", 3)

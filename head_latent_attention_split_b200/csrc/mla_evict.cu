@@ -469,6 +469,9 @@ mla_status_t mla_cache_compact(const mla_compact_params_t* p, void* kv_cache, vo
   const bool fp8 = p->cache_dtype == MLA_DTYPE_E4M3;
   if (fp8 ? (!kv_scale || (p->rope_dim > 0 && !k_rope_cache)) : (k_rope_cache || kv_scale)) return MLA_ERR_INVALID_ARG;
   if (block_table == dst_block_table) return MLA_ERR_INVALID_ARG;   // the destination blocks must be free
+  // (a weight moves while others are read: in place, one block's writes would meet another's reads)
+  if (mass && overlap(mass, 4ull * p->batch * p->mass_stride, mass_out, 4ull * p->batch * p->mass_out_stride))
+    return MLA_ERR_INVALID_ARG;
   const void* p4[] = {block_table, dst_block_table, indices, counts, mass, mass_out, kv_scale};
   for (const void* q : p4)
     if (q && !aligned(q, 4)) return MLA_ERR_ALIGNMENT;

@@ -83,6 +83,11 @@ cudaError_t launch_simt_decode(const DecodeArgs& a, cudaStream_t s);
 // Log-sum-exp merge of split partials (and the fill of empty sequences).
 cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t s);
 
+// Whether two buffers of so many bytes share one.
+inline bool overlap(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes) {
+  return (uintptr_t)a < (uintptr_t)b + b_bytes && (uintptr_t)b < (uintptr_t)a + a_bytes;
+}
+
 // Sticky status word of the current device (null when there is none).
 int* current_status_word();
 

@@ -444,7 +444,8 @@ mla_status_t mla_evict_select(const mla_evict_params_t* params, const float* mas
  * pool: entry j < counts[b] of indices[b] moves from the slot block_table maps it to, to slot j
  * through dst_block_table, with its latent, RoPE key and scale, byte for byte. When mass is
  * given, mass_out[b, j] = mass[b, indices[b,j]] and the rest of the row (counts[b] <= j <
- * mass_out_stride) becomes 0, so tokens appended later start without weight. counts[b] is the
+ * mass_out_stride) becomes 0, so tokens appended later start without weight. mass and mass_out may
+ * not overlap (MLA_ERR_INVALID_ARG). counts[b] is the
  * sequence's length under the new table; slots past it are left as they were.
  * The blocks of dst_block_table must be free: none of them may be named by a block table that
  * is still read (a shared prefix block can therefore stay shared with other sequences), and no two

@@ -1,0 +1,19 @@
+"""CPU-only: calls of the bounded-cache operators whose buffers overlap, or whose numbers leave the range that the
+kernels index in, are refused before anything is launched."""
+import pytest
+
+from test_bounded_host import FAKE, _compact, m  # noqa: F401
+
+F = 4   # bytes of a weight
+
+
+# mass [2, 192] and mass_out [2, 64]: one buffer for both, a first or last element in common
+@pytest.mark.parametrize("out", [FAKE, FAKE + 191 * F, FAKE + (2 * 192 - 1) * F, FAKE - (2 * 64 - 1) * F])
+def test_compact_refuses_weights_that_it_would_read_and_write(m, out):  # noqa: F811
+    assert _compact(m, mass=FAKE, mass_out=out) == 1
+
+
+# ... side by side (the call is refused for its list's alignment, checked later, and not before)
+@pytest.mark.parametrize("out", [FAKE + 2 * 192 * F, FAKE - 2 * 64 * F])
+def test_compact_takes_weights_side_by_side(m, out):  # noqa: F811
+    assert _compact(m, mass=FAKE, mass_out=out, indices=FAKE + 2) == 3
