@@ -422,7 +422,8 @@ mla_status_t mla_evict_select(const mla_evict_params_t* p, const float* mass, co
   if (!p || p->batch < 0 || p->max_seq_len < 0 || p->budget < 1 || p->sinks < 0 || p->recent < 0 ||
       (int64_t)p->sinks + p->recent > p->budget || p->reserved != 0)
     return MLA_ERR_INVALID_ARG;
-  if (p->max_seq_len > (1 << 30) || p->batch > (1 << 27)) return MLA_ERR_UNSUPPORTED;
+  // (32-bit counters step over the rows of mass and indices)
+  if (p->max_seq_len > (1 << 30) || p->budget > (1 << 30) || p->batch > (1 << 27)) return MLA_ERR_UNSUPPORTED;
   if (p->batch == 0) return MLA_OK;
   if (!mass || !seq_lens || !indices || !counts) return MLA_ERR_INVALID_ARG;
   const void* p4[] = {mass, seq_lens, indices, counts};
@@ -462,7 +463,8 @@ mla_status_t mla_cache_compact(const mla_compact_params_t* p, void* kv_cache, vo
   if ((mass == nullptr) != (mass_out == nullptr)) return MLA_ERR_INVALID_ARG;
   if (mass && (p->mass_stride < 1 || p->mass_out_stride < p->list_stride)) return MLA_ERR_INVALID_ARG;
   if ((int64_t)p->max_blocks_per_seq * p->block_size > (1ll << 30) || (int64_t)p->kv_rank + p->rope_dim > (1 << 20) ||
-      (int64_t)p->num_blocks * p->block_size > (1ll << 31) - 1)
+      (int64_t)p->num_blocks * p->block_size > (1ll << 31) - 1 || p->list_stride > (1 << 30) ||
+      (mass && (p->mass_stride > (1 << 30) || p->mass_out_stride > (1 << 30))))
     return MLA_ERR_UNSUPPORTED;
   if (p->batch == 0) return MLA_OK;
   if (!kv_cache || !block_table || !dst_block_table || !indices || !counts) return MLA_ERR_INVALID_ARG;

@@ -426,7 +426,7 @@ mla_status_t mla_attention_mass(const mla_decode_params_t* params, int32_t max_s
  * +0; a NaN ranks above every number). indices int32 [B, budget] gets the positions in ascending
  * order, -1 past the count; counts int32 [B] = min(seq_lens[b], budget): the list format of
  * mla_sparse_decode, which can attend over the kept tokens without moving them. mass f32
- * [B, max_seq_len]. sinks + recent <= budget, budget >= 1. A seq_len below 0 or above max_seq_len
+ * [B, max_seq_len]. sinks + recent <= budget, 1 <= budget <= 2^30, max_seq_len <= 2^30. A seq_len below 0 or above max_seq_len
  * sets MLA_ERR_BAD_SEQ_LEN and counts as 0. Asynchronous, allocates nothing. */
 typedef struct {
   int32_t batch;        /* B */
@@ -450,7 +450,7 @@ mla_status_t mla_evict_select(const mla_evict_params_t* params, const float* mas
  * The blocks of dst_block_table must be free: none of them may be named by a block table that
  * is still read (a shared prefix block can therefore stay shared with other sequences), and no two
  * sequences may share one. The copies run in no particular order.
- * Cache tensors and dtypes as in mla_decode; indices int32 [B, list_stride]; counts outside
+ * Cache tensors and dtypes as in mla_decode; strides up to 2^30; indices int32 [B, list_stride]; counts outside
  * [0, list_stride] are clamped and set MLA_ERR_BAD_SEQ_LEN; an entry whose position or block is
  * out of range is not copied, its mass becomes NaN, and MLA_ERR_BAD_BLOCK_ID is set. After
  * MLA_ERR_TIMEOUT some entries have not been copied. Asynchronous, allocates nothing. */

@@ -2,7 +2,7 @@
 kernels index in, are refused before anything is launched."""
 import pytest
 
-from test_bounded_host import FAKE, _compact, m  # noqa: F401
+from test_bounded_host import FAKE, _compact, _evict, m  # noqa: F401
 
 F = 4   # bytes of a weight
 
@@ -17,3 +17,19 @@ def test_compact_refuses_weights_that_it_would_read_and_write(m, out):  # noqa: 
 @pytest.mark.parametrize("out", [FAKE + 2 * 192 * F, FAKE - 2 * 64 * F])
 def test_compact_takes_weights_side_by_side(m, out):  # noqa: F811
     assert _compact(m, mass=FAKE, mass_out=out, indices=FAKE + 2) == 3
+
+
+# A row of more than 2^30 entries: the kernels' 32-bit loop counters would pass 2^31 and come back negative.
+BIG = (1 << 30) + 1
+
+
+@pytest.mark.parametrize("budget", [BIG, 2 ** 31 - 1])
+def test_select_refuses_a_budget_that_its_counters_cannot_pass(m, budget):  # noqa: F811
+    assert _evict(m, budget=budget) == 2
+
+
+@pytest.mark.parametrize("bad", [dict(list_stride=BIG, dst_max_blocks=1 << 25, mass=None, mass_out=None), dict(mass_out_stride=BIG),
+                                 dict(mass_out_stride=2 ** 31 - 1), dict(mass_stride=BIG)])
+def test_compact_refuses_rows_that_its_counters_cannot_pass(m, bad):  # noqa: F811
+    out = FAKE + (1 << 40)
+    assert _compact(m, **{**dict(mass=FAKE, mass_out=out), **bad}) == 2
