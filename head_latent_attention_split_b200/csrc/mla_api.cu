@@ -306,6 +306,8 @@ mla_status_t mla_attention_mass(const mla_decode_params_t* p, int32_t max_seq_le
   } else if (k_rope_cache || kv_scale) {
     return MLA_ERR_INVALID_ARG;
   }
+  const uint64_t mass_bytes = 4ull * p->batch * max_seq_len;
+  if (mass_in && mass_in != mass && mla::overlap(mass_in, mass_bytes, mass, mass_bytes)) return MLA_ERR_INVALID_ARG;
   const size_t need = kernel == MLA_KERNEL_SIMT ? 4 : 16;
   const void* ptrs[] = {q_lat, q_rope, kv_cache, k_rope_cache, kv_scale};
   for (const void* q : ptrs)

@@ -402,7 +402,7 @@ mla_status_t mla_window_decode(const mla_decode_params_t* params, int32_t window
  *                                exp(sigma_t(s,h) - lse[b,s,h]),        t < seq_lens[b],
  *
  * with mla_decode's scores, causal rule and lse output (so each row adds 1 over the sequence). All
- * sums are fp32, in a fixed order. mass_in may be NULL (zeros) or equal mass (no other overlap);
+ * sums are fp32, in a fixed order. mass_in may be NULL (zeros) or equal mass (any other overlap is refused);
  * entries t >= seq_lens[b] are not written. The caller keeps the entries of positions without a
  * token at 0, so that a token appended there starts without weight: after a verification that
  * shortens a sequence, set the refused drafts' entries to 0. mass_in, mass f32 [B, max_seq_len]; lse f32 [B, Sq, H].

@@ -2,7 +2,7 @@
 kernels index in, are refused before anything is launched."""
 import pytest
 
-from test_bounded_host import FAKE, _compact, _evict, m  # noqa: F401
+from test_bounded_host import FAKE, _compact, _evict, _mass, m  # noqa: F401
 
 F = 4   # bytes of a weight
 
@@ -33,3 +33,10 @@ def test_select_refuses_a_budget_that_its_counters_cannot_pass(m, budget):  # no
 def test_compact_refuses_rows_that_its_counters_cannot_pass(m, bad):  # noqa: F811
     out = FAKE + (1 << 40)
     assert _compact(m, **{**dict(mass=FAKE, mass_out=out), **bad}) == 2
+
+
+# mass_in may be mass itself; half on top of it, one row's sums would be another's start
+@pytest.mark.parametrize("mass_in,code", [(FAKE + F, 1), (FAKE - F, 1), (FAKE + (2 * 64 - 1) * F, 1),
+                                          (FAKE + 2 * 64 * F, 3), (FAKE, 3), (None, 3)])
+def test_attention_mass_refuses_a_start_that_overlaps_its_result(m, mass_in, code):  # noqa: F811
+    assert _mass(m, mass_in=mass_in, lse=FAKE + 2) == code   # (3: taken so far, refused for lse's alignment)
