@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "mla_internal.h"
+#include "ptx_sm100.cuh"
 #include "../../include/mla_decode.h"
 
 namespace mla {
@@ -31,11 +32,12 @@ __device__ __forceinline__ float e4m3_to_float(uint32_t code) {
   return (code & 0x80) ? -v : v;
 }
 
-// A bf16 row as two e4m3 rows, so that the FP8 tensor path multiplies it: x * 2^-e = hi + lo, with one
-// e per row chosen so that its largest magnitude lands in [128, 256). A bf16 value has 8 significant bits:
-// hi is the nearest value with 4, and x - hi is a multiple of the same last place with at most 4 of its
-// own, so hi + lo is exact down to 2^-10 of the row's largest magnitude; below, both meet e4m3's smallest
-// step (2^-9) and lose at most half of it each: 2^-9 / 128 = 2^-16 of that magnitude.
+// A bf16 row as an e4m3 and an e5m2 row, so that the FP8 tensor path multiplies it: x * 2^-e = hi + lo, with
+// one e per row chosen so that its largest magnitude lands in [128, 256). hi is the nearest e4m3 value (4
+// significant bits), lo the remainder behind it, in e5m2. A bf16 value has 8 significant bits, so the remainder
+// is 0 to 8 of its last places, which e5m2's 3 bits hold: hi + lo is exact from e4m3's smallest normal 2^-6
+// upward, 2^-13 of the row's largest magnitude. Below, the remainder is at most 2^-10 and lo off by 2^-14 at
+// most: 2^-14 / 128 = 2^-21 of that magnitude.
 __device__ __forceinline__ float bf16x2_amax(uint32_t v) {
   return fmaxf(fabsf(__uint_as_float(v << 16)), fabsf(__uint_as_float(v & 0xFFFF0000u)));
 }
@@ -47,18 +49,6 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// x to 4 significant bits, nearest (halves away from 0): an e4m3 value where it is not below e4m3's normal
-// range. (Integer arithmetic: conversions there and back run at a quarter of its rate or less.)
-__device__ __forceinline__ float top4(float x) { return __uint_as_float((__float_as_uint(x) + 0x80000u) & 0xFFF00000u); }
-// four values (two bf16 pairs) -> four hi codes and four lo codes; down = 2^-e
-__device__ __forceinline__ void split_e4m3(uint32_t v0, uint32_t v1, float down, uint32_t& hi, uint32_t& lo) {
-  const float x0 = __uint_as_float(v0 << 16) * down, x1 = __uint_as_float(v0 & 0xFFFF0000u) * down;
-  const float x2 = __uint_as_float(v1 << 16) * down, x3 = __uint_as_float(v1 & 0xFFFF0000u) * down;
-  const float h0 = top4(x0), h1 = top4(x1), h2 = top4(x2), h3 = top4(x3);
-  hi = f32x2_to_e4m3(h0, h1) | (f32x2_to_e4m3(h2, h3) << 16);
-  lo = f32x2_to_e4m3(x0 - h0, x1 - h1) | (f32x2_to_e4m3(x2 - h2, x3 - h3) << 16);
-}
-
 // Two e5m2 codes (2 mantissa bits, normal from 2^-14, smallest step 2^-16).
 __device__ __forceinline__ uint32_t f32x2_to_e5m2(float lo, float hi) {
   uint16_t r;
@@ -67,9 +57,31 @@ __device__ __forceinline__ uint32_t f32x2_to_e5m2(float lo, float hi) {
 }
 // The number c for which (x + c) - c is x to the nearest e4m3 value (|x| below 448): 1.5 * 2^20 times the
 // power of two at or below |x|, or times 2^-6, e4m3's smallest normal: c's last place is then that of x's
-// four significant bits, and 2^-9 for smaller x.
+// four significant bits, and 2^-9 for smaller x. (Arithmetic: conversions there and back run at a quarter
+// of its rate or less.)
 __device__ __forceinline__ float e4m3_rounder(float x) {
   return __uint_as_float(max(__float_as_uint(x) & 0x7F800000u, 121u << 23) + ((20u << 23) | 0x400000u));
+}
+// A pair of values (packed, see f2_pack) as two hi codes and two lo codes.
+__device__ __forceinline__ void two_terms(unsigned long long x2, uint32_t& hi, uint32_t& lo) {
+  const unsigned long long minus = ptx::f2_pack(-1.f, -1.f);
+  float x0, x1, h0, h1, l0, l1;
+  ptx::f2_unpack(x2, x0, x1);
+  const unsigned long long c2 = ptx::f2_pack(e4m3_rounder(x0), e4m3_rounder(x1));
+  const unsigned long long h2 = ptx::fma2(c2, minus, ptx::add2(x2, c2));   // hi's value
+  ptx::f2_unpack(h2, h0, h1);
+  ptx::f2_unpack(ptx::fma2(h2, minus, x2), l0, l1);
+  hi = f32x2_to_e4m3(h0, h1);
+  lo = f32x2_to_e5m2(l0, l1);
+}
+// four values (two bf16 pairs) -> four hi codes and four lo codes; down = 2^-e
+__device__ __forceinline__ void split_f8(uint32_t v0, uint32_t v1, float down, uint32_t& hi, uint32_t& lo) {
+  const unsigned long long d2 = ptx::f2_pack(down, down);
+  uint32_t h[2], l[2];
+  two_terms(ptx::mul2(ptx::f2_pack(__uint_as_float(v0 << 16), __uint_as_float(v0 & 0xFFFF0000u)), d2), h[0], l[0]);
+  two_terms(ptx::mul2(ptx::f2_pack(__uint_as_float(v1 << 16), __uint_as_float(v1 & 0xFFFF0000u)), d2), h[1], l[1]);
+  hi = h[0] | (h[1] << 16);
+  lo = l[0] | (l[1] << 16);
 }
 
 __device__ __forceinline__ float load_q(const void* p, int dtype, size_t i) {

@@ -16,7 +16,7 @@
 // runs of four tiles at a time (150 * 4 * 147 KB: the second group's reads hit L2); a token's sum over
 // the groups is added up by one thread, in order.
 // With an e4m3 cache the codes are an operand as they are (kind::f8f6f4): the bf16 query is split into
-// two e4m3 terms (8 = 4 + 4 significant bits, see split_e4m3), both multiplied into one accumulator,
+// an e4m3 and an e5m2 term (8 = 4 + 4 significant bits, see split_f8), both multiplied into one accumulator,
 // and the RoPE part has its own bf16 MMAs and accumulator since the token's scale does not apply to
 // it. No conversion of cache data at all.
 // Bound: memory. Per 128 tokens and SM 36 MMAs of N = 128 take about 2.9 k cycles and the
@@ -154,7 +154,7 @@ struct MassCtl {
 };
 static_assert(sizeof(MassCtl) <= kCtlBytes, "control block");
 
-// One query row (16 channels per lane, v = 8 bf16 pairs) as hi + lo e4m3 terms of x * 2^-e (split_e4m3);
+// One query row (16 channels per lane, v = 8 bf16 pairs) as hi + lo terms of x * 2^-e (split_f8);
 // returns the exponent field of 2^e.
 __device__ __forceinline__ uint32_t split_row(const uint32_t* v, uint32_t* hi, uint32_t* lo) {
   float m = 0.f;
@@ -165,7 +165,7 @@ __device__ __forceinline__ uint32_t split_row(const uint32_t* v, uint32_t* hi, u
   const int e = split_exponent(m);
   const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) split_e4m3(v[2 * i], v[2 * i + 1], down, hi[i], lo[i]);
+  for (int i = 0; i < 4; ++i) split_f8(v[2 * i], v[2 * i + 1], down, hi[i], lo[i]);
   return (uint32_t)(127 + e);
 }
 
@@ -318,7 +318,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA issuer (a converged warp)
     const bool leader = elect_one();
-    const uint32_t idesc16 = idesc_bf16_f32(kTile, N, false), idesc8 = idesc_e4m3_f32(kTile, N);
+    const uint32_t idesc16 = idesc_bf16_f32(kTile, N, false), idesc8 = idesc_e4m3_f32(kTile, N),
+                   idesc8lo = idesc_f8_f32(kTile, N, false, true);
     // operand descriptors of ring slot 0 and query chunk 0; a step of 32 bytes (K = 16 bf16 or 32 codes) adds 2
     const uint64_t ring_desc = smem_desc(sRing, 16, 1024, kSwizzle128B), q_desc = smem_desc(sQ, 16, 1024, kSwizzle128B);
     auto wait = [&](uint64_t& bar, uint32_t parity) {
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {   // hi then lo into the same accumulator
               mma_f8_ss(d, ad + 2 * kk, bd + 2 * kk, idesc8, (j | kk) ? 1u : 0u);
-              mma_f8_ss(d, ad + 2 * kk, lo + 2 * kk, idesc8, 1u);
+              mma_f8_ss(d, ad + 2 * kk, lo + 2 * kk, idesc8lo, 1u);
             }
           } else {
             const uint32_t dd = kFp8 ? d + kGroupRows : d;   // e4m3: RoPE scores in their own columns

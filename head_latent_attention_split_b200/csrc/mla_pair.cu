@@ -37,11 +37,12 @@
 //
 // kFp8 (window decode over an e4m3 cache): the codes are MMA operands as they are, in both CTAs; nothing
 // is converted per tile.
-//   scores: the query is split into two e4m3 terms (split_e4m3) that fill 256 TMEM columns; both multiply
+//   scores: the query is split into an e4m3 and an e5m2 term (split_f8) that fill 256 TMEM columns; both multiply
 //     every 128-channel chunk of codes into one accumulator, and the RoPE parts (bf16, the query's in
 //     shared memory) have a second one, since a token's scale applies to the latent part only:
-//     score = 2^e (acc s_t + rope), the query's power of two in the row's softmax scale. 36 MMAs per tile pair,
-//     as with a bf16 cache.
+//     score = 2^e (acc s_t + rope), the query's power of two in the row's softmax scale. e is the latent part's
+//     (its terms are what has few bits), unless the RoPE part, in bf16, is 2^64 times as large. 36 MMAs per tile
+//     pair, as with a bf16 cache.
 //   probabilities: w = P s_t as hi = e4m3(w) and lo = e5m2(w - hi), the remainder behind the stored hi, so the
 //     PV is 8 MMAs per tile on the codes themselves. The remainder of 4 significant bits is at most half of
 //     the fourth one, and e5m2's three hold it to 2^-8 of w, a bf16 rounding's accuracy, from e4m3's smallest
@@ -424,6 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc2 = idesc_bf16_f32(128, 128, false);   // a tile pair
     constexpr uint32_t idesc1 = idesc_bf16_f32(128, 64, false);    // a single tile
     constexpr uint32_t idesc2c = idesc_e4m3_f32(128, 128), idesc1c = idesc_e4m3_f32(128, 64);
+    constexpr uint32_t idesc2l = idesc_f8_f32(128, 128, true, false), idesc1l = idesc_f8_f32(128, 64, true, false);   // lo
     // descriptor of ring slot 0's rows (K-major, 8-row groups 1 KB apart, the second tile right after the
     // first); 32 bytes along K add 2
     const uint64_t ring_desc = smem_desc(smem_u32(smem + kOffRingS), 16, 1024, kSwizzle128B);
@@ -454,11 +456,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if constexpr (kFp8) {
               if (g < kChunksS8 - 1) {
                 // 32 channels per step: eight TMEM columns of codes; hi, then lo into the same accumulator
-                const uint32_t qa = tmem + kTmemQ + 32 * g, ic = two ? idesc2c : idesc1c;
+                const uint32_t qa = tmem + kTmemQ + 32 * g, ic = two ? idesc2c : idesc1c, il = two ? idesc2l : idesc1l;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                   mma_f8_ts(tmem + kTmemS8, qa + 8 * kk, bdesc + 2 * kk, ic, (g | kk) ? 1u : 0u);
-                  mma_f8_ts(tmem + kTmemS8, qa + kTmemLo8 + 8 * kk, bdesc + 2 * kk, ic, 1u);
+                  mma_f8_ts(tmem + kTmemS8, qa + kTmemLo8 + 8 * kk, bdesc + 2 * kk, il, 1u);
                 }
               } else {
 #pragma unroll
@@ -574,11 +576,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                              fmaxf(bf16x2_amax(q[k][i].z), bf16x2_amax(q[k][i].w))));
             }
             start();
-            if (half == 1) {
+            if (half == 1) {   // (the RoPE part as 2^-64 of itself: bf16 keeps its bits under any e, as long as sums stay finite)
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                mx[i] = fmaxf(mx[i], fmaxf(fmaxf(bf16x2_amax(n0[i].x), bf16x2_amax(n0[i].y)),
-                                           fmaxf(bf16x2_amax(n0[i].z), bf16x2_amax(n0[i].w))));
+                mx[i] = fmaxf(mx[i], 0x1p-64f * fmaxf(fmaxf(bf16x2_amax(n0[i].x), bf16x2_amax(n0[i].y)),
+                                                     fmaxf(bf16x2_amax(n0[i].z), bf16x2_amax(n0[i].w))));
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -605,7 +607,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (k < 4) {   // 64 channels as 16 words of hi codes and 16 of lo
                 uint32_t hl[32];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) split_e4m3(w32[2 * i], w32[2 * i + 1], down, hl[i], hl[16 + i]);
+                for (int i = 0; i < 16; ++i) split_f8(w32[2 * i], w32[2 * i + 1], down, hl[i], hl[16 + i]);
                 tmem_st16(tmem + lane_off + kTmemQ + 64 * half + 16 * k, hl);
                 tmem_st16(tmem + lane_off + kTmemQ + kTmemLo8 + 64 * half + 16 * k, hl + 16);
               } else {       // RoPE channels, scaled alike: 128 bytes of the K-major operand, 128-byte swizzle
@@ -784,19 +786,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const int j = 4 * k + 2 * h;
-                  float x0, x1, w0, w1, l0, l1;
+                  float x0, x1;
                   f2_unpack(fma2(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), cc, nm), x0, x1);
                   const unsigned long long p2 = f2_pack(ex2_approx(x0), ex2_approx(x1));
                   acc = add2(acc, p2);
-                  const unsigned long long w2 = mul2(p2, h ? s4.y : s4.x);
-                  f2_unpack(w2, w0, w1);
-                  const unsigned long long c2 = f2_pack(e4m3_rounder(w0), e4m3_rounder(w1)), minus = f2_pack(-1.f, -1.f);
-                  const unsigned long long h2 = fma2(c2, minus, add2(w2, c2));   // hi's value
-                  float h0, h1;
-                  f2_unpack(h2, h0, h1);
-                  f2_unpack(fma2(h2, minus, w2), l0, l1);
-                  hi[h] = f32x2_to_e4m3(h0, h1);
-                  lo[h] = f32x2_to_e5m2(l0, l1);
+                  two_terms(mul2(p2, h ? s4.y : s4.x), hi[h], lo[h]);
                 }
                 pk[k] = hi[0] | (hi[1] << 16);
                 pk[16 + k] = lo[0] | (lo[1] << 16);

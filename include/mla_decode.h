@@ -381,7 +381,7 @@ mla_status_t mla_sparse_decode(const mla_decode_params_t* params, int32_t top_k,
  * bad lengths and blocks are mla_decode's; the sequences' RoPE keys keep the positions they were
  * rotated for. Kernels: mla_decode's, and MLA_KERNEL_TC_PAIR takes an E4M3 cache too (AUTO's choice
  * for it): the query and the weights then go to the FP8 tensor path as two 8-bit terms each. The query's
- * error is at most 2^-16 of its row's largest magnitude (RoPE part included). A weight times its token's scale
+ * error is at most 2^-21 of its row's largest latent magnitude (its RoPE part stays bf16). A weight times its token's scale
  * is held to 2^-8 of itself, as with a bf16 cache; what is small against its neighbours may lose more, but all
  * that such weights of a row lose together stays below 2^-8 + 2^-9 of the row's sum, however many they are. (TCGEN05 holds
  * them as mla_decode does: in fp16, the row's largest weight as 1 to 2^8, so that a weight times its scale
@@ -413,8 +413,8 @@ mla_status_t mla_window_decode(const mla_decode_params_t* params, int32_t window
  * out (MLA_ERR_TIMEOUT) get NaN. Asynchronous, allocates nothing.
  *
  * TCGEN05 with an E4M3 cache multiplies the codes as they are and splits each bf16 query value
- * into two e4m3 terms, x = hi + lo, scaled by a power of two per row: exact for values within
- * 2^-10 of the row's largest magnitude, off by at most 2^-16 of that magnitude below it. */
+ * into an e4m3 and an e5m2 term, x = hi + lo, scaled by a power of two per row: exact for values within
+ * 2^-13 of the row's largest magnitude, off by at most 2^-21 of that magnitude below it. */
 mla_status_t mla_attention_mass(const mla_decode_params_t* params, int32_t max_seq_len, const void* q_lat,
                                 const void* q_rope, const void* kv_cache, const void* k_rope_cache,
                                 const float* kv_scale, const int32_t* block_table, const int32_t* seq_lens,
