@@ -490,8 +490,9 @@ mla_status_t mla_cache_compact(const mla_compact_params_t* params, void* kv_cach
  *
  * Products, differences and sums are fp64 (the sums in a fixed order). draft NULL: the drafts were
  * not sampled (greedy, n-gram), q_i is 1 at x_i and 0 elsewhere. w counts as 0 where it is not
- * above 0 (NaN included). sample_u is clamped into [0, 1): a value of 1 or more draws the last
- * token with a weight, a negative or NaN one the first. Rows past i = accepted are not read.
+ * above 0 (NaN included). sample_u is clamped to [0, 1 - 2^-24]: a value of 1 or more acts as 1 - 2^-24
+ * (not as the last token with a weight, where what follows adds up to less than 2^-24 of the sum), a
+ * negative or NaN one as 0, which draws the first token with a weight. Rows past i = accepted are not read.
  * target [B, K + 1, V], draft [B, K, V] of type prob_dtype (F32 or BF16); draft_tokens int32
  * [B, K]; accept_u f32 [B, K]; sample_u f32 [B]; tokens int32 [B, K + 1]; accepted int32 [B];
  * seq_lens and new_seq_lens int32 [B], both or neither. new_seq_lens may equal seq_lens.
