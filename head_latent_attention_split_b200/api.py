@@ -81,7 +81,9 @@ def cache_append(c_new, k_rope_new, kv_cache, block_table, seq_lens, k_rope_cach
     kv_cache [num_blocks, block_size, r + d_r] (f32 / bf16), or e4m3 codes
     [num_blocks, block_size, r] (uint8) with k_rope_cache bf16 [num_blocks, block_size, d_r]
     and kv_scale float32 [num_blocks, block_size]. Token s of sequence b lands at position
-    seq_lens[b] - Sq + s. With rope, the RoPE key is rotated for that position first.
+    seq_lens[b] - Sq + s. With rope, the RoPE key is rotated for that position first (not for a cache that
+    cache_compact has cut: its kept keys have the rotations of the whole sequence, so rotate the new ones for
+    their places there and leave rope off).
     """
     B, Sq, r = c_new.shape
     d_r = k_rope_new.shape[-1] if k_rope_new is not None else 0
@@ -360,7 +362,9 @@ def cache_compact(kv_cache, block_table, dst_block_table, indices, counts, k_rop
                   mass_out=None, stream=None):
     """Copy the listed tokens into the (free) blocks of dst_block_table, in list order (see
     mla_cache_compact): counts are the sequences' lengths under the new table. With mass and mass_out
-    (two buffers) the tokens' weights move along, and the rest of each mass_out row becomes 0. Returns None."""
+    (two buffers) the tokens' weights move along, and the rest of each mass_out row becomes 0. The RoPE keys
+    stay rotated for the positions the tokens had: cache_append then takes rope=False and keys rotated for
+    their places in the whole sequence. Returns None."""
     import torch
     dev = _cuda_device(kv_cache, "kv_cache")
     nb, bs, width = _dims(kv_cache, "kv_cache", 3)

@@ -254,6 +254,9 @@ const char* mla_status_string(int32_t status);
  *   - rope != 0: the RoPE key is rotated before it is stored: pairs (x[2i], x[2i+1]) turn by
  *     pos * theta_i with theta_i = rope_base^(-2i / d_r) (angle and rotation in fp64, result
  *     rounded to the cache type). rope == 0 stores k_rope_new as given (already rotated).
+ *     The position is the slot's: behind an eviction (mla_cache_compact) it is no longer the token's
+ *     place in the sequence, which the kept keys stay rotated for, so such a cache takes rope == 0 and
+ *     keys that the caller has rotated for their places in the whole sequence.
  *
  * c_new [B, Sq, r] and k_rope_new [B, Sq, d_r] have type in_dtype; all pointers are device
  * pointers; the call is asynchronous on `stream` and allocates nothing. Argument errors
@@ -452,7 +455,9 @@ mla_status_t mla_evict_select(const mla_evict_params_t* params, const float* mas
  * sequences may share one. The copies run in no particular order.
  * Cache tensors and dtypes as in mla_decode; strides up to 2^30; indices int32 [B, list_stride]; counts outside
  * [0, list_stride] are clamped and set MLA_ERR_BAD_SEQ_LEN; an entry whose position or block is
- * out of range is not copied, its mass becomes NaN, and MLA_ERR_BAD_BLOCK_ID is set. After
+ * out of range is not copied, its mass becomes NaN, and MLA_ERR_BAD_BLOCK_ID is set. The RoPE keys
+ * stay rotated for the positions the tokens had: append further tokens with rope == 0 and keys rotated
+ * for their places in the whole sequence, which the caller counts (counts[b] no longer says it). After
  * MLA_ERR_TIMEOUT some entries have not been copied. Asynchronous, allocates nothing. */
 typedef struct {
   int32_t batch;            /* B */
