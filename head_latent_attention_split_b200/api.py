@@ -256,7 +256,15 @@ def _step(q_lat, q_rope, kv_cache, block_table, seq_lens, softmax_scale, causal,
                           _b.int32(num_workers, "num_workers"), _b.KERNELS[kernel] if isinstance(kernel, str) else kernel, 0)
 
 
-_workspace_bytes = {}   # (device, parameters) -> mla_decode_workspace_size, a function of nothing else
+_workspace_bytes = {}   # (device, parameters) -> _window_workspace, a function of nothing else
+
+
+def _window_workspace(p):
+    """Bytes that a window decode of these parameters needs."""
+    if p.cache_dtype == _b.E4M3 and p.kernel == _b.KERNELS["tc_pair"]:   # sized as the decode's own e4m3 kernel
+        p = _b.Params.from_buffer_copy(p)
+        p.kernel = _b.KERNELS["tcgen05"]
+    return max(_b.workspace_size(p), 1)
 
 
 def window_decode(q_lat, q_rope, kv_cache, block_table, seq_lens, softmax_scale, window, sinks=0, causal=False,
@@ -292,7 +300,7 @@ def window_decode(q_lat, q_rope, kv_cache, block_table, seq_lens, softmax_scale,
         if n is None:
             if len(_workspace_bytes) >= 4096:
                 _workspace_bytes.clear()
-            n = _workspace_bytes[key] = max(_b.workspace_size(p), 1)
+            n = _workspace_bytes[key] = _window_workspace(p)
         workspace = torch.empty_strided((n,), (1,), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the device of q_lat")

@@ -186,8 +186,7 @@ mla_status_t mla_decode_resolve(const mla_decode_params_t* p, int32_t* kernel, i
 mla_status_t mla_decode_workspace_size(const mla_decode_params_t* p, size_t* bytes) {
   if (!bytes) return MLA_ERR_INVALID_ARG;
   int k = 0, W = 0;
-  // (window: its kernels for these parameters have the same layout and worker count, and one more of them)
-  mla_status_t st = resolve(p, &k, &W, false, true);
+  mla_status_t st = resolve(p, &k, &W);
   if (st) return st;
   *bytes = layout_for(p, W).total;
   return MLA_OK;

@@ -380,7 +380,8 @@ mla_status_t mla_sparse_decode(const mla_decode_params_t* params, int32_t top_k,
  * counts once. window >= 1, sinks >= 0; values past the block table's capacity act as the
  * capacity. A window of at least the sequence's length is mla_decode's definition, and by the same
  * kernel its result (for an E4M3 cache AUTO takes another one here). out, lse, the other
- * arguments, the workspace (mla_decode_workspace_size of the same params) and the handling of
+ * arguments, the workspace (mla_decode_workspace_size of the same params; for TC_PAIR with an E4M3 cache, which
+ * mla_decode refuses, of the params with TCGEN05: the two need the same) and the handling of
  * bad lengths and blocks are mla_decode's; the sequences' RoPE keys keep the positions they were
  * rotated for. Kernels: mla_decode's, and MLA_KERNEL_TC_PAIR takes an E4M3 cache too (AUTO's choice
  * for it): the query and the weights then go to the FP8 tensor path as two 8-bit terms each. The query's

@@ -40,3 +40,21 @@ def test_compact_refuses_rows_that_its_counters_cannot_pass(m, bad):  # noqa: F8
                                           (FAKE + 2 * 64 * F, 3), (FAKE, 3), (None, 3)])
 def test_attention_mass_refuses_a_start_that_overlaps_its_result(m, mass_in, code):  # noqa: F811
     assert _mass(m, mass_in=mass_in, lse=FAKE + 2) == code   # (3: taken so far, refused for lse's alignment)
+
+
+def test_workspace_size_answers_for_the_calls_that_the_decode_takes(m):  # noqa: F811
+    # the decode has no split-role kernel for an e4m3 cache, so there is no size for it either
+    shape = dict(B=2, Sq=1, H=128, r=512, d_r=64, block_size=64, num_blocks=2, max_blocks_per_seq=1, q_dtype=1, out_dtype=1,
+                 causal=False, softmax_scale=0.2, num_workers=74)
+    p = m.make_params(**shape, cache_dtype=2, kernel="tc_pair")
+    with pytest.raises(m.MlaError) as e:
+        m.workspace_size(p)
+    assert e.value.status == 2
+    # the window decode, which has one, is sized as by the decode's kernel and takes exactly that
+    from head_latent_attention_split_b200 import api
+    need = api._window_workspace(p)
+    assert need == m.workspace_size(m.make_params(**shape, cache_dtype=2, kernel="tcgen05")) and p.kernel == m.KERNELS["tc_pair"]
+    ptrs = dict(q_lat=FAKE, q_rope=FAKE, kv_cache=FAKE, k_rope_cache=FAKE, kv_scale=FAKE, block_table=FAKE, seq_lens=FAKE,
+                out=FAKE + 8, lse=FAKE, workspace=FAKE)
+    call = lambda n: m.mla_window_decode(p, 16, 2, stream=0, check=False, workspace_bytes=n, **ptrs)  # noqa: E731
+    assert call(need - 1) == 4 and call(need) == 3   # too small; enough, and then refused for out's alignment
