@@ -451,15 +451,23 @@ cudaError_t launch_simt_decode(const DecodeArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t s) {
-  // Up to two blocks per SM with one per eight rows: latency decides (32 e4m3 window sequences of 34 tiles: 72.5 us,
-  // 75.0 with the other variant at three per SM). Beyond, occupancy does: 128 x 256 rows of a ragged batch
-  // merge in 24.6 us with 61 registers, 36.9 with 118. A dense batch then keeps a block per eight rows, since its
-  // sequences' splits differ (30.7 us when four per SM walk the rows); the blocks of a window batch walk
-  // them, since its splits are alike and often single (133 us a step, 141 otherwise).
-  constexpr int kSms = 148;
+  // Up to two blocks per SM with one per eight rows: latency decides, and the variant of 118 registers has the first
+  // partials under way early. Beyond, resident warps do, with 61 registers. A step with the one and the other, us
+  // (sequences x rows, from a cold L2; the rule's side first):
+  //   up to two: window 16 x 32 39.3, 41.0; 1 x 128 of 65 tiles 43.0, 47.2; 8 x 128 51.2, 53.4; dense 18 x 128 80.3, 82.0;
+  //   beyond: window 24 x 128 70.0, 72.2; 32 x 128 e4m3 83.5, 86.1; 96 ragged x 256 145.4, 151.6; dense 24 ragged x 128
+  //   59.6, 61.6; 128 ragged x 256 159.7, 170.6; but window 30 ragged x 256 69.6, 68.2.
+  // Beyond, a dense batch keeps a block per eight rows, since its sequences' splits differ (128 ragged x 256: 159.7,
+  // 163.9 when four blocks per SM walk the rows; 64 x 128: 178.1, 176.1). The blocks of a window batch walk them:
+  // there it is a draw (30 ragged x 256: 69.6, 71.6 with a block per eight rows; 96 ragged x 256 145.4 both; 40
+  // ragged x 128 90.0, 86.0), and blocks of sequences that need no merge are fewer.
+  int dev = 0, sms = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (err != cudaSuccess) return err;
   const int groups = (a.rows + kWarps - 1) / kWarps, batch = std::max(a.B, 1);
-  const bool many = (int64_t)groups * batch > 2 * kSms;
-  const int walk = std::max(1, std::min(groups, (many ? 4 : 2) * kSms / batch));
+  const bool many = (int64_t)groups * batch > 2 * sms;
+  const int walk = std::max(1, std::min(groups, (many ? 4 : 2) * sms / batch));
   const dim3 grid(a.B, many && a.window == 0 ? groups : walk);
   if (a.window > 0) {
     // a dependent of the decode kernel before it: its blocks may start while that kernel's last CTAs run
