@@ -153,7 +153,7 @@ struct WindowTiles {
   //   a longest share 12 tiles above the even one: 15 x 257: 109, -, 109;
   //   one worker or less per sequence: 64 x 65: 129, 111; 40 x 33: 77, 70; 80 x 8: 67, 57; 80 x 17: 80, 81.
   // The same thresholds serve fewer rows and the e4m3 cache. Over 28 such batches (1 to 300 sequences, windows of 60
-  // to 4096) with 8 and 128 rows, bf16 and e4m3, the even cut takes 0.84 to 1.38 times this rule's time, 1.09 in the
+  // to 4096) with 8 and 128 rows, bf16 and e4m3, the even cut takes 0.84 to 1.38 times this rule's time, 1.08 in the
   // mean: 70 x 8 e4m3 1.30 (8 rows), 1.28 (128); 300 x 2 1.00, 1.38; but 80 x 17 0.84 (8 rows, 0.98 with 128), where
   // few rows leave no merge to save, and 50 x 65 0.89, 0.98.
   // Where nothing is hidden the cut stays the dense one, and with it the result.
