@@ -58,14 +58,14 @@
 //     Down steps cost what the up steps do, a pass over O: at scores of deviation 1.7, 33 pairs make 6 up and
 //     2 down steps per warp.
 //   Half the bytes per tile: twice the ring slots.
-//   Bound by the softmax warps, 3.4 us per tile pair at 128 rows (bf16 2.3): scores and scales 1.05,
-//   exponentials and the two terms 1.15, the message 0.55, the rest waiting; a segment's start costs
+//   Bound by the softmax warps, 3.3 us per tile pair at 128 rows (bf16 2.3): scores and scales 1.1,
+//   exponentials and the two terms 1.3, the message 0.55, the rest waiting; a segment's start costs
 //   another 11 us, most of it the query's split.
 //
 // kWindow: the tile list holds only the blocks that some row sees (WindowTiles), the softmax masks what a
 // row does not see of them, and the cut among the workers is WindowTiles::cut's. 128 heads, bf16: 64
 // sequences x 65 tiles in 100 us (3.1 TB/s of cache, 42 % of the tensor pipe's time); 96 sequences x 256 causal
-// rows, windows of 1500: 132 us; e4m3, 32 x 34 tiles: 72 us. Bound by the coupled latencies of the tile loop
+// rows, windows of 1500: 132 us; e4m3, 32 x 34 tiles: 73 us. Bound by the coupled latencies of the tile loop
 // (2.3 us per pair, of which the 36 score MMAs 1.4) and by a segment's 14 us around it.
 #include <cuda.h>
 
@@ -749,14 +749,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           bool move = mt > m_run + kRescaleThreshold;   // the reference moves
           float m_new = kFp8 ? mt - kHeadroom8 : mt;
           if constexpr (kFp8) {
-            if (move) {
-              m_top = fmaxf(m_top, m_new);
-            } else if (mt < m_run + kLow8 && mt > -INFINITY && m_run > m_top - kDepth8) {
+            const bool is_low = mt < m_run + kLow8 && mt > -INFINITY && m_run > m_top - kDepth8;
+            if (move) m_top = fmaxf(m_top, m_new);
+            if (is_low) {
               ++low;
               low_max = fmaxf(low_max, mt);
             }
-            // one row's turn lowers all of the warp's rows with low pairs (both halves decide alike)
-            if (__any_sync(0xffffffffu, low >= kLowPairs8) && low > 0 && !move) {
+            // one row's turn lowers those of the warp whose pair is low too (both halves decide alike)
+            if (__any_sync(0xffffffffu, low >= kLowPairs8) && is_low) {
               move = true;
               m_new = fmaxf(low_max - kHeadroom8, m_top - kDepth8);
             }

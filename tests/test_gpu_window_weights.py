@@ -142,3 +142,17 @@ def test_a_sink_among_tokens_of_unlike_magnitudes():
     levels = [sink(math.log(n)), sink(math.log(9 * n)), noisy(math.log(n), 1.0, 2), noisy(0.0, 0.5, 2)]
     check(build(n, levels, 16, amp=amp), n, 0)
     check(build(n, levels, 16, amp=amp * 2.0 ** -12), 3000, 1)
+
+
+@pytest.mark.parametrize("back", [0.0, 2.0, 3.0, 4.0])
+@pytest.mark.parametrize("workers", [1, 0])
+def test_one_rows_turn_leaves_its_neighbours_large_weights(back, workers):
+    """Rows beside one another: one of a sink over a flat tail, the others low too but for one pair of tiles, each
+    another one, where their scores come back to the first token's level (and `back` above it)."""
+    n = 64 * 50
+    pair = lambda t: t // 128  # noqa: E731
+    levels = [sink(14.0)] + [(lambda t, j=j: (14.0 + back * (t > 0)) * ((t == 0) | (pair(t) == j)).double()) for j in range(1, 21)]
+    check(build(n, levels, 32), n, 0, num_workers=workers)
+    levels = [noisy(14.0, 0.3, 4)] + [(lambda t, j=j: (14.0 + back * (t > 0)) * ((t == 0) | (t == 128 * j + 77)).double()
+                                       - 9.0 * (pair(t) % 3 == 1)) for j in range(4, 24)]
+    check(build(n, levels, 21, Sq=2), n, 0, causal=True, num_workers=workers)
