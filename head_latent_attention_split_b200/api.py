@@ -314,7 +314,7 @@ def attention_mass(q_lat, q_rope, kv_cache, block_table, seq_lens, lse, softmax_
     """mass[b, t] = mass_in[b, t] + the attention weight that token t receives from all query rows
     of this step, for t < seq_lens[b] (see mla_attention_mass).
 
-    lse [B, Sq, H] is the decode's; mass float32 [B, max_seq_len]; mass_in of the same shape, or mass
+    lse [B, Sq, H] is the decode's over the whole cache (not window_decode's); mass float32 [B, max_seq_len]; mass_in of the same shape, or mass
     itself to add in place, or None for zeros. Entries past a sequence's length are left as they are.
     Returns mass.
     """

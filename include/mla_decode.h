@@ -405,7 +405,8 @@ mla_status_t mla_window_decode(const mla_decode_params_t* params, int32_t window
  *     mass[b,t] = mass_in[b,t] + sum over the rows (s, h) that see token t of
  *                                exp(sigma_t(s,h) - lse[b,s,h]),        t < seq_lens[b],
  *
- * with mla_decode's scores, causal rule and lse output (so each row adds 1 over the sequence). All
+ * with mla_decode's scores, causal rule and lse output (so each row adds 1 over the sequence; there is no
+ * form for a window: mla_window_decode's lse would give weight to tokens that no row saw). All
  * sums are fp32, in a fixed order. mass_in may be NULL (zeros) or equal mass (any other overlap is refused);
  * entries t >= seq_lens[b] are not written. The caller keeps the entries of positions without a
  * token at 0, so that a token appended there starts without weight: after a verification that
@@ -452,8 +453,8 @@ mla_status_t mla_evict_select(const mla_evict_params_t* params, const float* mas
  * not overlap (MLA_ERR_INVALID_ARG). counts[b] is the
  * sequence's length under the new table; slots past it are left as they were.
  * The blocks of dst_block_table must be free: none of them may be named by a block table that
- * is still read (a shared prefix block can therefore stay shared with other sequences), and no two
- * sequences may share one. The copies run in no particular order.
+ * is still read (a shared prefix block can therefore stay shared with other sequences), and none may be
+ * named twice, by one sequence or by two. The copies run in no particular order.
  * Cache tensors and dtypes as in mla_decode; strides up to 2^30; indices int32 [B, list_stride]; counts outside
  * [0, list_stride] are clamped and set MLA_ERR_BAD_SEQ_LEN; an entry whose position or block is
  * out of range is not copied, its mass becomes NaN, and MLA_ERR_BAD_BLOCK_ID is set. The RoPE keys
