@@ -22,7 +22,7 @@
 // Bound: memory. Per 128 tokens and SM 36 MMAs of N = 128 take about 2.9 k cycles and the
 // exponentials about 1.1 k (16 per cycle), the tile's bytes at 1/148 of the HBM rate 6.4 k (bf16)
 // or 3.6 k (e4m3). Measured at 128 heads: bf16, 64 sequences of 8192: 111 us (5.4 TB/s; up to 124 us in long
-// runs under the power cap); e4m3, 48 sequences of up to 16384: 63 us (2.9 TB/s). What is missing is
+// runs under the power cap); e4m3, 48 sequences of up to 16384: 64 us (2.8 TB/s). What is missing is
 // the ring: 80 KB in flight per SM beside the query, at about 2.2 us of latency under load, and with an
 // e4m3 cache the start of each sequence's tiles behind its query. An L2 prefetch of the blocks ahead made it
 // slower (117 to 122 us and more), other L2 promotion sizes changed nothing.

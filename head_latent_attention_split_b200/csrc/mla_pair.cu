@@ -65,7 +65,7 @@
 // kWindow: the tile list holds only the blocks that some row sees (WindowTiles), the softmax masks what a
 // row does not see of them, and the cut among the workers is WindowTiles::cut's. 128 heads, bf16: 64
 // sequences x 65 tiles in 100 us (3.1 TB/s of cache, 42 % of the tensor pipe's time); 96 sequences x 256 causal
-// rows, windows of 1500: 132 us; e4m3, 32 x 33 tiles: 73 us. Bound by the coupled latencies of the tile loop
+// rows, windows of 1500: 132 us; e4m3, 32 x 33 tiles: 74 us. Bound by the coupled latencies of the tile loop
 // (2.3 us per pair, of which the 36 score MMAs 1.4) and by a segment's 14 us around it.
 #include <cuda.h>
 
