@@ -79,7 +79,7 @@ def load_peaks():
 # only holds for the sources the kernel was built from, keyed here by kernel and the SHA-256 prefix of
 # those files; for any other source the bench reports traffic as null.
 MEASURED_TRAFFIC = {
-    ("tc_pair", "b42f8e88e411e882"): {"deepseek_v3": (304.367872e6 + 5.932544e6) / 262144},
+    ("tc_pair", "604fe415067c6752"): {"deepseek_v3": (304.426240e6 + 5.497600e6) / 262144},
 }
 KERNEL_SOURCES = {
     "tc_pair": ("mla_pair.cu", "ptx_sm100.cuh", "mla_device.cuh", "mla_internal.h", "mla_tc.h"),
@@ -88,7 +88,7 @@ KERNEL_SOURCES = {
 # The same for the sparse step's indexer (dram bytes per context token, batch 8 of the
 # 128K workload), keyed by the sources of mla_dsa.cu and its headers.
 DSA_TRAFFIC = {
-    "1d72216b1b3fb8f4": {"dsa_v32": (138.622720e6 + 4.129280e6) / (8 * 131072)},
+    "6be3e91db5bfe6d7": {"dsa_v32": (138.622208e6 + 4.231936e6) / (8 * 131072)},
 }
 DSA_SOURCES = ("mla_dsa.cu", "ptx_sm100.cuh", "mla_device.cuh", "mla_internal.h")
 
